@@ -186,8 +186,10 @@ spava_status spava_prefill_attention_host(const spava_config *cfg, const void *q
                                           void *copy_stream);
 
 /* Synchronises `stream`, reads the workspace status word (bit 0: a bounded wait
- * in a kernel gave up), writes it to *flags and clears it.  Returns
- * SPAVA_ERR_TIMEOUT if bit 0 was set, SPAVA_OK otherwise. */
+ * in a kernel gave up; bit 1: a spava_cache_* call met a length or a page
+ * outside its table or pool), writes it to *flags and clears it.  Returns
+ * SPAVA_ERR_TIMEOUT if bit 0 was set, SPAVA_ERR_INVALID_ARG if only bit 1 was,
+ * SPAVA_OK otherwise. */
 spava_status spava_device_status(void *ws, size_t ws_bytes, void *stream, int32_t *flags);
 
 /* Self-test of the failure path (the pages have no counterpart): launches one
@@ -329,6 +331,154 @@ spava_status spava_score_noalloc(const spava_config *cfg, const void *q, const v
  * up, the scores are incomplete), writes it to *flags and clears it.  Returns
  * SPAVA_ERR_TIMEOUT if bit 0 was set, SPAVA_OK otherwise.  Allocates nothing. */
 spava_status spava_score_noalloc_status(void *stream, int32_t *flags);
+
+/* ---------------------------------------------------------------------------
+ * The answering side: what a model runs around the prefill layer above.  (The
+ * pages take post-rotary Q and K and stop at the prefill; these operators make
+ * those inputs and answer from what the prefill leaves behind.)
+ *
+ *   spava_qk_norm_rope  RMS norm of every query and key head and the position
+ *                       rotation, in one pass: the Q and K of a layer
+ *   spava_cache_write   a layer's K and V rows into a paged cache, as bf16 or
+ *                       quantised to e4m3
+ *   spava_cache_append  both for new tokens: q normed and rotated, k normed,
+ *                       rotated and cached, v cached, in one launch
+ *   spava_cache_read    cached rows back as contiguous bf16
+ *   spava_cache_attn    attention of one new token per sequence over the cache
+ *
+ * The conventions at the head of this file hold.  These calls may be captured
+ * into CUDA graphs.  The current device must be the one of the buffers and the
+ * stream.
+ * ------------------------------------------------------------------------- */
+
+/* For a token at position p (one per axis) and a head row x of d elements:
+ *   y = x * w / sqrt(mean(x^2) + eps)            (norm 1; norm 0: y = x)
+ *   pair j < rope_dim/2: angle = p[axis(j)] * inv_freq[j],
+ *     (y_a, y_b) -> (y_a cos - y_b sin, y_b cos + y_a sin)
+ * and one rounding to bf16 at the end.  Angles are reduced in 64 bits, so far
+ * positions keep their accuracy. */
+typedef struct {
+    int32_t n_q_heads;   /* Hq: 1..4096 */
+    int32_t n_kv_heads;  /* Hkv >= 1, Hq % Hkv == 0 */
+    int32_t head_dim;    /* d: 64 or 128 */
+    int32_t rope_dim;    /* rotated elements, the first of the head: 0 or a multiple
+                            of 16 up to d; the others pass through */
+    int32_t interleaved; /* 0: pair j = elements (j, j + rope_dim/2); 1: (2j, 2j+1) */
+    int32_t n_axes;      /* position axes: 1..4 */
+    int32_t section[4];  /* the first section[0] pairs turn by axis 0's position, the
+                            next section[1] by axis 1's, ...; >= 0, the first n_axes
+                            sum to rope_dim/2 */
+    int32_t norm;        /* 1: RMS norm; 0: none (eps and the weights are not used) */
+    float eps;           /* >= 0 */
+} spava_rope_config;
+
+/* q [n_rows, Hq, d] and k [n_rows, Hkv, d] bf16, heads contiguous, tokens
+ * q_stride and k_stride elements apart (at least Hq*d and Hkv*d, multiples of
+ * 8: views of one fused projection are fine).  q_weight, k_weight: bf16 [d]
+ * (NULL: ones).  inv_freq: float32 [rope_dim/2] (may be NULL if rope_dim is 0).
+ * positions: int32 [n_axes, n_rows] (may be NULL if rope_dim is 0).
+ * Writes q_out [n_rows, Hq, d] and k_out [n_rows, Hkv, d] contiguous; either
+ * may be its input itself (same address, contiguous stride) and must not
+ * overlap an input otherwise.  n_rows 0 is allowed and does nothing. */
+spava_status spava_qk_norm_rope(const spava_rope_config *cfg, int64_t n_rows, const void *q,
+                                int64_t q_stride, const void *k, int64_t k_stride,
+                                const void *q_weight, const void *k_weight, const float *inv_freq,
+                                const int32_t *positions, void *q_out, void *k_out, void *stream);
+
+typedef enum {
+    SPAVA_CACHE_BF16 = 0,
+    SPAVA_CACHE_E4M3 = 1 /* e4m3 values with one int8 exponent per row */
+} spava_cache_type;
+
+/* A paged cache of one layer's keys and values.  Position t of a sequence lies
+ * in row t % page_size of page table[t / page_size]. */
+typedef struct {
+    int32_t n_q_heads;  /* Hq (spava_cache_attn) */
+    int32_t n_kv_heads; /* Hkv; Hq % Hkv == 0 */
+    int32_t head_dim;   /* d: 64 or 128 */
+    int32_t page_size;  /* rows per page: 1..65536 */
+    int64_t n_pages;    /* >= 1; n_pages * Hkv * page_size < 2^32 - 1 */
+    int32_t type;       /* a spava_cache_type */
+    float scale;        /* softmax scale; <= 0 selects 1/sqrt(d) */
+} spava_cache_config;
+
+/* The caller's pools: k, v [n_pages, Hkv, page_size, d], bf16 or e4m3; for
+ * e4m3 also k_exp, v_exp, int8 [n_pages, Hkv, page_size] (else not used).  A
+ * row x is held as round_e4m3(x * 2^-e) and e, the smallest e >= -120 with
+ * max|x| <= 448 * 2^e over its finite elements (-120 for a row of zeros): a
+ * power of two leaves every significand as it is, so the row's only rounding
+ * is the one to e4m3.  NaN and infinities are held as NaN. */
+typedef struct {
+    void *k;
+    void *v;
+    int8_t *k_exp;
+    int8_t *v_exp;
+} spava_cache_pools;
+
+/* A batch of sequences, all DEVICE memory (so that a captured graph can be
+ * replayed with other contents): table int32 [n_seqs, max_pages] and lens int32
+ * [n_seqs], the tokens of each sequence, new ones included.  max_pages >= 1,
+ * max_pages * page_size < 2^31, n_seqs < 2^20.  Table entries behind the last
+ * page of a sequence are not read.  Sequences may share pages.  A length below
+ * 0 counts as 0, one beyond the table as the table's end; a page outside the
+ * pool is neither read nor written, its positions count as absent; each of the
+ * three sets bit 1 of the workspace status word. */
+typedef struct {
+    int64_t n_seqs;
+    int64_t max_pages;
+    const int32_t *table;
+    const int32_t *lens;
+} spava_cache_batch;
+
+/* Workspace bytes of the spava_cache_* calls for this config, whatever the
+ * batch.  256-byte aligned, ZERO at first, used by spava_cache_* calls (and
+ * spava_device_status) alone: it holds counters that every call returns to
+ * zero.  Calls that share it must be ordered (on one stream, or by events). */
+spava_status spava_cache_workspace_size(const spava_cache_config *cfg, size_t *bytes);
+
+/* Writes new_rows rows of every sequence, its last ones: row i of sequence b
+ * (token b * new_rows + i of k and v) goes to position lens[b] - new_rows + i;
+ * rows whose position would be negative are skipped.  k, v: [n_seqs *
+ * new_rows, Hkv, d] bf16, tokens k_stride and v_stride elements apart (as in
+ * spava_qk_norm_rope).  Two rows that go to one place of the pool leave
+ * unspecified contents there.  Nothing else in the pools changes. */
+spava_status spava_cache_write(const spava_cache_config *cfg, const spava_cache_pools *pools,
+                               const spava_cache_batch *batch, int64_t new_rows, const void *k,
+                               int64_t k_stride, const void *v, int64_t v_stride, void *ws,
+                               size_t ws_bytes, void *stream);
+
+/* spava_qk_norm_rope and spava_cache_write of its k_out and of v in one launch,
+ * byte for byte: q_out [n_seqs * new_rows, Hq, d]; positions int32 [n_axes,
+ * n_seqs * new_rows] are those of the rotation.  Head counts and head_dim of
+ * both configs must agree. */
+spava_status spava_cache_append(const spava_rope_config *rope, const spava_cache_config *cfg,
+                                const spava_cache_pools *pools, const spava_cache_batch *batch,
+                                int64_t new_rows, const void *q, int64_t q_stride, const void *k,
+                                int64_t k_stride, const void *v, int64_t v_stride,
+                                const void *q_weight, const void *k_weight, const float *inv_freq,
+                                const int32_t *positions, void *q_out, void *ws, size_t ws_bytes,
+                                void *stream);
+
+/* Positions [first, first + rows) of every sequence as bf16, k_out and v_out
+ * [n_seqs, rows, Hkv, d]: e4m3 rows as value * 2^e (exact in bf16; infinite
+ * where e4m3 rounded a value next to bf16's largest up past it); zeros from
+ * position lens[b] on.  first >= 0, first + rows < 2^31. */
+spava_status spava_cache_read(const spava_cache_config *cfg, const spava_cache_pools *pools,
+                              const spava_cache_batch *batch, int64_t first, int64_t rows,
+                              void *k_out, void *v_out, void *ws, size_t ws_bytes, void *stream);
+
+/* Attention of one query token per sequence, q [n_seqs, Hq, d] bf16, over the
+ * sequence's positions [0, lens[b]):
+ *   o[b, h] = sum_t softmax_t(scale * q[b, h] . k[t, h / (Hq/Hkv)]) v[t]
+ * o [n_seqs, Hq, d] bf16; lse (may be NULL) float32 [Hq, n_seqs], natural log:
+ * with it, partial results over parts of a context can be merged.  A sequence
+ * without positions gives o = 0 and lse = -inf.  Positions past lens[b] are
+ * never read, whatever they hold.  Several new tokens of one sequence are
+ * several rows of the batch, with the same table row and growing lens.
+ * Results do not depend on timing: the same call gives the same bytes. */
+spava_status spava_cache_attn(const spava_cache_config *cfg, const spava_cache_pools *pools,
+                              const spava_cache_batch *batch, const void *q, void *o, float *lse,
+                              void *ws, size_t ws_bytes, void *stream);
 
 const char *spava_status_string(spava_status s);
 

@@ -17,7 +17,7 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libspava.so")
-SOURCES = [os.path.join(CSRC, "spava_api.cu")]
+SOURCES = [os.path.join(CSRC, f) for f in ("spava_api.cu", "cache_api.cu")]
 DEPS = SOURCES + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + [
     os.path.join(ROOT, "include", "spava.h")]
 

@@ -1,0 +1,339 @@
+// cache_api.cu -- the C ABI's answering side (include/spava.h): argument checks
+// and launches of the norm/rotation, paged cache and one-token attention
+// kernels.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <atomic>
+#include <cmath>
+
+#include "../../include/spava.h"
+#include "cache_common.cuh"
+#include "decode_kernel.cuh"
+#include "row_kernels.cuh"
+#include "status.cuh"
+
+using namespace spava;
+
+namespace {
+
+spava_status check_heads(int32_t Hq, int32_t Hkv, int32_t d) {
+    if (Hq < 1 || Hkv < 1 || d < 1 || Hq % Hkv) return SPAVA_ERR_INVALID_ARG;
+    if (d != 64 && d != 128) return SPAVA_ERR_UNSUPPORTED;
+    if (Hq > 4096) return SPAVA_ERR_UNSUPPORTED;
+    return SPAVA_OK;
+}
+
+spava_status check_rope(const spava_rope_config *c) {
+    if (!c) return SPAVA_ERR_INVALID_ARG;
+    SPAVA_TRY(check_heads(c->n_q_heads, c->n_kv_heads, c->head_dim));
+    if (c->rope_dim < 0 || c->rope_dim > c->head_dim) return SPAVA_ERR_INVALID_ARG;
+    if (c->rope_dim % 2) return SPAVA_ERR_INVALID_ARG;
+    if (c->rope_dim % 16) return SPAVA_ERR_UNSUPPORTED;
+    if (c->interleaved != 0 && c->interleaved != 1) return SPAVA_ERR_INVALID_ARG;
+    if (c->norm != 0 && c->norm != 1) return SPAVA_ERR_INVALID_ARG;
+    if (c->norm && !(c->eps >= 0.f && std::isfinite(c->eps))) return SPAVA_ERR_INVALID_ARG;
+    if (c->n_axes < 1) return SPAVA_ERR_INVALID_ARG;
+    if (c->n_axes > 4) return SPAVA_ERR_UNSUPPORTED;
+    int64_t sum = 0;
+    for (int a = 0; a < c->n_axes; ++a) {
+        if (c->section[a] < 0) return SPAVA_ERR_INVALID_ARG;
+        sum += c->section[a];
+    }
+    return sum == c->rope_dim / 2 ? SPAVA_OK : SPAVA_ERR_INVALID_ARG;
+}
+
+spava_status check_cache(const spava_cache_config *c) {
+    if (!c) return SPAVA_ERR_INVALID_ARG;
+    SPAVA_TRY(check_heads(c->n_q_heads, c->n_kv_heads, c->head_dim));
+    if (c->page_size < 1 || c->n_pages < 1) return SPAVA_ERR_INVALID_ARG;
+    if (c->type != SPAVA_CACHE_BF16 && c->type != SPAVA_CACHE_E4M3) return SPAVA_ERR_INVALID_ARG;
+    if (c->page_size > 65536) return SPAVA_ERR_UNSUPPORTED;
+    if (!std::isfinite(c->scale)) return SPAVA_ERR_INVALID_ARG;
+    const int64_t per_page = int64_t(c->n_kv_heads) * c->page_size;
+    if (c->n_pages > (int64_t(kNoRow) - 1) / per_page) return SPAVA_ERR_UNSUPPORTED;
+    return SPAVA_OK;
+}
+
+// A token source: heads contiguous, tokens `stride` elements apart.
+spava_status check_rows(const void *p, int64_t stride, int heads, int d) {
+    SPAVA_TRY(check_ptr(p));
+    if (stride < int64_t(heads) * d) return SPAVA_ERR_INVALID_ARG;
+    return stride % 8 ? SPAVA_ERR_MISALIGNED : SPAVA_OK;
+}
+
+constexpr size_t kCounterBytes = (sizeof(int32_t) * kDecMaxCtas + 255) / 256 * 256;
+
+int head_tile(const spava_cache_config *c) { return c->n_q_heads / c->n_kv_heads > 8 ? 2 : 1; }
+
+// [status block 256 | counters | partial statistics | partial O]
+size_t cache_ws_bytes(const spava_cache_config *c) {
+    const size_t heads = 8 * head_tile(c);
+    return 256 + kCounterBytes + sizeof(float) * 2 * kDecMaxCtas * heads * (3 + c->head_dim);
+}
+
+spava_status make_view(const spava_cache_config *c, const spava_cache_pools *p,
+                       const spava_cache_batch *b, void *ws, size_t ws_bytes, CacheView *v) {
+    SPAVA_TRY(check_cache(c));
+    if (!p || !b) return SPAVA_ERR_INVALID_ARG;
+    if (b->n_seqs < 0 || b->max_pages < 1) return SPAVA_ERR_INVALID_ARG;
+    if (b->n_seqs >= (1LL << 20)) return SPAVA_ERR_UNSUPPORTED;
+    if (b->max_pages >= ((1LL << 31) + c->page_size - 1) / c->page_size) return SPAVA_ERR_UNSUPPORTED;
+    SPAVA_TRY(check_ptr(p->k));
+    SPAVA_TRY(check_ptr(p->v));
+    if (c->type == SPAVA_CACHE_E4M3 && (!p->k_exp || !p->v_exp)) return SPAVA_ERR_INVALID_ARG;
+    if (!b->table || !b->lens) return SPAVA_ERR_INVALID_ARG;
+    if ((reinterpret_cast<uintptr_t>(b->table) & 3) || (reinterpret_cast<uintptr_t>(b->lens) & 3))
+        return SPAVA_ERR_MISALIGNED;
+    if (!ws) return SPAVA_ERR_WORKSPACE;
+    if (reinterpret_cast<uintptr_t>(ws) & 255) return SPAVA_ERR_MISALIGNED;
+    if (ws_bytes < cache_ws_bytes(c)) return SPAVA_ERR_WORKSPACE;
+    v->k = p->k;
+    v->v = p->v;
+    v->k_exp = p->k_exp;
+    v->v_exp = p->v_exp;
+    v->table = b->table;
+    v->lens = b->lens;
+    v->status = static_cast<int *>(ws);
+    v->max_pages = b->max_pages;
+    v->n_pages = static_cast<uint32_t>(std::min<int64_t>(c->n_pages, INT32_MAX));
+    v->n_seqs = static_cast<int32_t>(b->n_seqs);
+    v->Hkv = c->n_kv_heads;
+    v->cap = static_cast<int32_t>(b->max_pages * c->page_size);
+    v->page = FastDiv::of(static_cast<uint32_t>(c->page_size));
+    return SPAVA_OK;
+}
+
+template <int CACHE>
+spava_status launch_rows(RowParams &p, int d, cudaStream_t st) {
+    const int64_t heads = int64_t(p.Hq) + p.Hk + p.Hv;
+    if (p.n_rows == 0) return SPAVA_OK;
+    if (p.n_rows >= (1LL << 31) / heads) return SPAVA_ERR_UNSUPPORTED;
+    p.n_items = static_cast<uint32_t>(p.n_rows * heads);
+    p.heads = FastDiv::of(static_cast<uint32_t>(heads));
+    const uint32_t per_block = kRowThreads / (d / 16);
+    const unsigned grid = (p.n_items + per_block - 1) / per_block;
+    if (d == 64)
+        row_kernel<64, CACHE><<<grid, kRowThreads, 0, st>>>(p);
+    else
+        row_kernel<128, CACHE><<<grid, kRowThreads, 0, st>>>(p);
+    return launched();
+}
+
+spava_status set_rope(const spava_rope_config *c, RowParams *p, const void *q_weight,
+                      const void *k_weight, const float *inv_freq, const int32_t *positions) {
+    if (c->norm) {
+        SPAVA_TRY(check_ptr(q_weight, false));
+        SPAVA_TRY(check_ptr(k_weight, false));
+    }
+    if (c->rope_dim > 0) {
+        if (!inv_freq || !positions) return SPAVA_ERR_INVALID_ARG;
+        if ((reinterpret_cast<uintptr_t>(inv_freq) & 3) || (reinterpret_cast<uintptr_t>(positions) & 3))
+            return SPAVA_ERR_MISALIGNED;
+    }
+    p->q_weight = static_cast<const __nv_bfloat16 *>(q_weight);
+    p->k_weight = static_cast<const __nv_bfloat16 *>(k_weight);
+    p->inv_freq = inv_freq;
+    p->positions = positions;
+    p->rope_dim = c->rope_dim;
+    p->interleaved = c->interleaved;
+    p->norm = c->norm;
+    p->eps = c->eps;
+    int32_t cut[4], at = 0;
+    for (int a = 0; a < 4; ++a) cut[a] = a < c->n_axes ? (at += c->section[a]) : INT32_MAX;
+    // the last axis in use ends at rope_dim / 2: no pair lies behind it
+    p->cut1 = cut[0];
+    p->cut2 = cut[1];
+    p->cut3 = cut[2];
+    return SPAVA_OK;
+}
+
+spava_status check_batch_rows(const spava_cache_batch *b, int64_t new_rows) {
+    if (new_rows < 0) return SPAVA_ERR_INVALID_ARG;
+    if (new_rows >= (1LL << 31)) return SPAVA_ERR_UNSUPPORTED;
+    return SPAVA_OK;
+}
+
+template <typename K>
+spava_status set_dynamic_smem(K kernel, int bytes, std::atomic<uint64_t> &done, int dev) {
+    // once a device: the attribute belongs to the function there
+    const uint64_t bit = dev < 64 ? 1ULL << dev : 0;
+    if (bit && (done.load(std::memory_order_acquire) & bit)) return SPAVA_OK;
+    SPAVA_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
+    done.fetch_or(bit, std::memory_order_release);
+    return SPAVA_OK;
+}
+
+template <int D, bool E4M3, int NT>
+spava_status launch_decode(DecodeParams &p, cudaStream_t st) {
+    static std::atomic<uint64_t> done{0};
+    int dev = 0, n_sm = 0;
+    SPAVA_CUDA(cudaGetDevice(&dev));
+    SPAVA_CUDA(cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev));
+    constexpr int smem = DecodeShape<D, E4M3, NT>::SMEM;
+    SPAVA_TRY(set_dynamic_smem(decode_kernel<D, E4M3, NT>, smem, done, dev));
+    const int grid = std::min(2 * n_sm, kDecMaxCtas);
+    decode_kernel<D, E4M3, NT><<<grid, kDecThreads, smem, st>>>(p);
+    return launched();
+}
+
+}  // namespace
+
+extern "C" {
+
+spava_status spava_qk_norm_rope(const spava_rope_config *cfg, int64_t n_rows, const void *q,
+                                int64_t q_stride, const void *k, int64_t k_stride,
+                                const void *q_weight, const void *k_weight, const float *inv_freq,
+                                const int32_t *positions, void *q_out, void *k_out, void *stream) {
+    SPAVA_TRY(check_rope(cfg));
+    if (n_rows < 0) return SPAVA_ERR_INVALID_ARG;
+    if (n_rows == 0) return SPAVA_OK;
+    SPAVA_TRY(check_rows(q, q_stride, cfg->n_q_heads, cfg->head_dim));
+    SPAVA_TRY(check_rows(k, k_stride, cfg->n_kv_heads, cfg->head_dim));
+    SPAVA_TRY(check_ptr(q_out));
+    SPAVA_TRY(check_ptr(k_out));
+    RowParams p{};
+    SPAVA_TRY(set_rope(cfg, &p, q_weight, k_weight, inv_freq, positions));
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    p.k_out = static_cast<__nv_bfloat16 *>(k_out);
+    p.n_rows = n_rows;
+    p.Hq = cfg->n_q_heads;
+    p.Hk = cfg->n_kv_heads;
+    return launch_rows<0>(p, cfg->head_dim, static_cast<cudaStream_t>(stream));
+}
+
+spava_status spava_cache_workspace_size(const spava_cache_config *cfg, size_t *bytes) {
+    if (!bytes) return SPAVA_ERR_INVALID_ARG;
+    SPAVA_TRY(check_cache(cfg));
+    *bytes = cache_ws_bytes(cfg);
+    return SPAVA_OK;
+}
+
+spava_status spava_cache_write(const spava_cache_config *cfg, const spava_cache_pools *pools,
+                               const spava_cache_batch *batch, int64_t new_rows, const void *k,
+                               int64_t k_stride, const void *v, int64_t v_stride, void *ws,
+                               size_t ws_bytes, void *stream) {
+    RowParams p{};
+    SPAVA_TRY(make_view(cfg, pools, batch, ws, ws_bytes, &p.cache));
+    SPAVA_TRY(check_batch_rows(batch, new_rows));
+    if (new_rows == 0 || batch->n_seqs == 0) return SPAVA_OK;
+    SPAVA_TRY(check_rows(k, k_stride, cfg->n_kv_heads, cfg->head_dim));
+    SPAVA_TRY(check_rows(v, v_stride, cfg->n_kv_heads, cfg->head_dim));
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.n_rows = batch->n_seqs * new_rows;
+    p.new_rows = FastDiv::of(static_cast<uint32_t>(new_rows));
+    p.Hk = p.Hv = cfg->n_kv_heads;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cfg->type == SPAVA_CACHE_E4M3 ? launch_rows<2>(p, cfg->head_dim, st)
+                                         : launch_rows<1>(p, cfg->head_dim, st);
+}
+
+spava_status spava_cache_append(const spava_rope_config *rope, const spava_cache_config *cfg,
+                                const spava_cache_pools *pools, const spava_cache_batch *batch,
+                                int64_t new_rows, const void *q, int64_t q_stride, const void *k,
+                                int64_t k_stride, const void *v, int64_t v_stride,
+                                const void *q_weight, const void *k_weight, const float *inv_freq,
+                                const int32_t *positions, void *q_out, void *ws, size_t ws_bytes,
+                                void *stream) {
+    SPAVA_TRY(check_rope(rope));
+    RowParams p{};
+    SPAVA_TRY(make_view(cfg, pools, batch, ws, ws_bytes, &p.cache));
+    if (rope->n_q_heads != cfg->n_q_heads || rope->n_kv_heads != cfg->n_kv_heads ||
+        rope->head_dim != cfg->head_dim)
+        return SPAVA_ERR_INVALID_ARG;
+    SPAVA_TRY(check_batch_rows(batch, new_rows));
+    if (new_rows == 0 || batch->n_seqs == 0) return SPAVA_OK;
+    SPAVA_TRY(check_rows(q, q_stride, cfg->n_q_heads, cfg->head_dim));
+    SPAVA_TRY(check_rows(k, k_stride, cfg->n_kv_heads, cfg->head_dim));
+    SPAVA_TRY(check_rows(v, v_stride, cfg->n_kv_heads, cfg->head_dim));
+    SPAVA_TRY(check_ptr(q_out));
+    SPAVA_TRY(set_rope(rope, &p, q_weight, k_weight, inv_freq, positions));
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.k = static_cast<const __nv_bfloat16 *>(k);
+    p.v = static_cast<const __nv_bfloat16 *>(v);
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.q_out = static_cast<__nv_bfloat16 *>(q_out);
+    p.n_rows = batch->n_seqs * new_rows;
+    p.new_rows = FastDiv::of(static_cast<uint32_t>(new_rows));
+    p.Hq = cfg->n_q_heads;
+    p.Hk = p.Hv = cfg->n_kv_heads;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    return cfg->type == SPAVA_CACHE_E4M3 ? launch_rows<2>(p, cfg->head_dim, st)
+                                         : launch_rows<1>(p, cfg->head_dim, st);
+}
+
+spava_status spava_cache_read(const spava_cache_config *cfg, const spava_cache_pools *pools,
+                              const spava_cache_batch *batch, int64_t first, int64_t rows,
+                              void *k_out, void *v_out, void *ws, size_t ws_bytes, void *stream) {
+    ReadParams p{};
+    SPAVA_TRY(make_view(cfg, pools, batch, ws, ws_bytes, &p.cache));
+    if (first < 0 || rows < 0) return SPAVA_ERR_INVALID_ARG;
+    if (first >= (1LL << 31) || rows >= (1LL << 31) || first + rows >= (1LL << 31))
+        return SPAVA_ERR_UNSUPPORTED;
+    if (rows == 0 || batch->n_seqs == 0) return SPAVA_OK;
+    SPAVA_TRY(check_ptr(k_out));
+    SPAVA_TRY(check_ptr(v_out));
+    const int64_t heads = cfg->n_kv_heads;
+    if (batch->n_seqs * rows >= (1LL << 31) / heads) return SPAVA_ERR_UNSUPPORTED;
+    p.k_out = static_cast<__nv_bfloat16 *>(k_out);
+    p.v_out = static_cast<__nv_bfloat16 *>(v_out);
+    p.first = static_cast<int32_t>(first);
+    p.n_items = static_cast<uint32_t>(batch->n_seqs * rows * heads);
+    p.rows = FastDiv::of(static_cast<uint32_t>(rows));
+    p.heads = FastDiv::of(static_cast<uint32_t>(heads));
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool e4m3 = cfg->type == SPAVA_CACHE_E4M3;
+    const uint32_t per_block = kRowThreads / (cfg->head_dim * (e4m3 ? 1 : 2) / 16);
+    const unsigned grid = (p.n_items + per_block - 1) / per_block;
+    if (cfg->head_dim == 64) {
+        if (e4m3) read_kernel<64, true><<<grid, kRowThreads, 0, st>>>(p);
+        else read_kernel<64, false><<<grid, kRowThreads, 0, st>>>(p);
+    } else {
+        if (e4m3) read_kernel<128, true><<<grid, kRowThreads, 0, st>>>(p);
+        else read_kernel<128, false><<<grid, kRowThreads, 0, st>>>(p);
+    }
+    return launched();
+}
+
+spava_status spava_cache_attn(const spava_cache_config *cfg, const spava_cache_pools *pools,
+                              const spava_cache_batch *batch, const void *q, void *o, float *lse,
+                              void *ws, size_t ws_bytes, void *stream) {
+    DecodeParams p{};
+    SPAVA_TRY(make_view(cfg, pools, batch, ws, ws_bytes, &p.cache));
+    if (batch->n_seqs == 0) return SPAVA_OK;
+    SPAVA_TRY(check_ptr(q));
+    SPAVA_TRY(check_ptr(o));
+    if (reinterpret_cast<uintptr_t>(lse) & 3) return SPAVA_ERR_MISALIGNED;
+    const int nt = head_tile(cfg);
+    p.q = static_cast<const __nv_bfloat16 *>(q);
+    p.o = static_cast<__nv_bfloat16 *>(o);
+    p.lse = lse;
+    p.Hq = cfg->n_q_heads;
+    p.G = cfg->n_q_heads / cfg->n_kv_heads;
+    p.n_hg = (p.G + 8 * nt - 1) / (8 * nt);
+    const double scale = cfg->scale > 0.f ? double(cfg->scale) : 1.0 / std::sqrt(double(cfg->head_dim));
+    p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
+    char *at = static_cast<char *>(ws) + 256;
+    p.counters = reinterpret_cast<int *>(at);
+    p.part_stat = reinterpret_cast<float *>(at + kCounterBytes);
+    p.part_o = p.part_stat + size_t(2) * kDecMaxCtas * 3 * 8 * nt;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const bool e4m3 = cfg->type == SPAVA_CACHE_E4M3;
+    if (cfg->head_dim == 64) {
+        if (e4m3) return nt == 1 ? launch_decode<64, true, 1>(p, st) : launch_decode<64, true, 2>(p, st);
+        return nt == 1 ? launch_decode<64, false, 1>(p, st) : launch_decode<64, false, 2>(p, st);
+    }
+    if (e4m3) return nt == 1 ? launch_decode<128, true, 1>(p, st) : launch_decode<128, true, 2>(p, st);
+    return nt == 1 ? launch_decode<128, false, 1>(p, st) : launch_decode<128, false, 2>(p, st);
+}
+
+}  // extern "C"

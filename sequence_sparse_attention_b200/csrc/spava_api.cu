@@ -16,31 +16,11 @@
 #include "score_kernel.cuh"
 #include "select_kernels.cuh"
 #include "shard_kernels.cuh"
+#include "status.cuh"
 
 using namespace spava;
 
 namespace {
-
-thread_local int32_t g_last_cuda_error = 0;
-
-spava_status cuda_fail(cudaError_t e) {
-    g_last_cuda_error = static_cast<int32_t>(e);
-    return SPAVA_ERR_CUDA;
-}
-
-spava_status cuda_ok(cudaError_t e) { return e == cudaSuccess ? SPAVA_OK : cuda_fail(e); }
-
-#define SPAVA_CUDA(...)                                    \
-    do {                                                   \
-        cudaError_t e_ = (__VA_ARGS__);                           \
-        if (e_ != cudaSuccess) return cuda_fail(e_);       \
-    } while (0)
-
-#define SPAVA_TRY(...)                                     \
-    do {                                                   \
-        spava_status s_ = (__VA_ARGS__);                          \
-        if (s_ != SPAVA_OK) return s_;                     \
-    } while (0)
 
 // ---------------------------------------------------------------- config
 spava_status make_layer(const spava_config *c, Layer *L) {
@@ -203,11 +183,6 @@ spava_status check_ws(const Layer &L, void *ws, size_t ws_bytes) {
 // that may run at the same time as another attention launch take slots 1 and 2.
 int *queue_slot(char *ws, int slot) { return reinterpret_cast<int *>(ws + 128 + 32 * slot); }
 
-spava_status check_ptr(const void *p, bool required = true) {
-    if (!p) return required ? SPAVA_ERR_INVALID_ARG : SPAVA_OK;
-    return (reinterpret_cast<uintptr_t>(p) & 15) ? SPAVA_ERR_MISALIGNED : SPAVA_OK;
-}
-
 // ---------------------------------------------------------------- TMA maps
 typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
                                   const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
@@ -266,11 +241,6 @@ template <typename K>
 spava_status set_smem(K kernel, int bytes) {
     SPAVA_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes));
     return SPAVA_OK;
-}
-
-spava_status launched() {
-    cudaError_t e = cudaGetLastError();
-    return e == cudaSuccess ? SPAVA_OK : cuda_fail(e);
 }
 
 // ---------------------------------------------------------------- launches
@@ -940,7 +910,8 @@ spava_status spava_device_status(void *ws, size_t ws_bytes, void *stream, int32_
         SPAVA_CUDA(cudaStreamSynchronize(st));
     }
     *flags = h;
-    return (h & kStatusTimeout) ? SPAVA_ERR_TIMEOUT : SPAVA_OK;
+    if (h & kStatusTimeout) return SPAVA_ERR_TIMEOUT;
+    return (h & kStatusBadBatch) ? SPAVA_ERR_INVALID_ARG : SPAVA_OK;
 }
 
 spava_status spava_selftest_wait_timeout(void *ws, size_t ws_bytes, void *stream) {

@@ -23,7 +23,9 @@ EXPORTS = ("spava_workspace_size", "spava_packed_len", "spava_score", "spava_top
            "spava_status_string", "spava_last_cuda_error", "spava_score_noalloc",
            "spava_selftest_wait_timeout", "spava_plan_chunks", "spava_score_noalloc_status",
            "spava_shard_layout", "spava_shard_sizes", "spava_shard_front", "spava_shard_local_attn",
-           "spava_shard_context_attn", "spava_shard_merge")
+           "spava_shard_context_attn", "spava_shard_merge", "spava_qk_norm_rope",
+           "spava_cache_workspace_size", "spava_cache_write", "spava_cache_append",
+           "spava_cache_read", "spava_cache_attn")
 
 
 class SpavaConfig(ctypes.Structure):
@@ -42,6 +44,32 @@ class SpavaConfig(ctypes.Structure):
         ("local_pair_full", ctypes.c_int32), ("score_norm", ctypes.c_int32),
         ("score_pool", ctypes.c_int32),
     ]
+
+
+class SpavaRopeConfig(ctypes.Structure):
+    """Mirror of ``spava_rope_config``."""
+    _fields_ = [("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("rope_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("n_axes", ctypes.c_int32),
+                ("section", ctypes.c_int32 * 4), ("norm", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class SpavaCacheConfig(ctypes.Structure):
+    """Mirror of ``spava_cache_config``."""
+    _fields_ = [("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int64), ("type", ctypes.c_int32),
+                ("scale", ctypes.c_float)]
+
+
+class SpavaCachePools(ctypes.Structure):
+    """Mirror of ``spava_cache_pools``."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p),
+                ("v_exp", ctypes.c_void_p)]
+
+
+class SpavaCacheBatch(ctypes.Structure):
+    """Mirror of ``spava_cache_batch``."""
+    _fields_ = [("n_seqs", ctypes.c_int64), ("max_pages", ctypes.c_int64), ("table", ctypes.c_void_p),
+                ("lens", ctypes.c_void_p)]
 
 
 class SpavaError(RuntimeError):
@@ -87,6 +115,17 @@ def load() -> ctypes.CDLL:
         "spava_shard_local_attn": [cfgp, i32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "spava_shard_context_attn": [cfgp, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp],
         "spava_shard_merge": [cfgp, i32, i32, vp, vp, vp, vp, sz, vp],
+    }
+    i64 = ctypes.c_int64
+    rope = ctypes.POINTER(SpavaRopeConfig)
+    cache = [ctypes.POINTER(SpavaCacheConfig), ctypes.POINTER(SpavaCachePools), ctypes.POINTER(SpavaCacheBatch)]
+    sig |= {
+        "spava_qk_norm_rope": [rope, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, vp],
+        "spava_cache_workspace_size": [cache[0], szp],
+        "spava_cache_write": [*cache, i64, vp, i64, vp, i64, vp, sz, vp],
+        "spava_cache_append": [rope, *cache, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, vp, sz, vp],
+        "spava_cache_read": [*cache, i64, i64, vp, vp, vp, sz, vp],
+        "spava_cache_attn": [*cache, vp, vp, vp, vp, sz, vp],
     }
     for name, args in sig.items():
         f = getattr(lib, name)
