@@ -418,7 +418,7 @@ typedef struct {
 /* A batch of sequences, all DEVICE memory (so that a captured graph can be
  * replayed with other contents): table int32 [n_seqs, max_pages] and lens int32
  * [n_seqs], the tokens of each sequence, new ones included.  max_pages >= 1,
- * max_pages * page_size < 2^31, n_seqs < 2^20.  Table entries behind the last
+ * max_pages * page_size <= 2^31 - 2^16, n_seqs < 2^20.  Table entries behind the last
  * page of a sequence are not read.  Sequences may share pages.  A length below
  * 0 counts as 0, one beyond the table as the table's end; a page outside the
  * pool is neither read nor written, its positions count as absent; each of the
@@ -475,7 +475,9 @@ spava_status spava_cache_read(const spava_cache_config *cfg, const spava_cache_p
  * without positions gives o = 0 and lse = -inf.  Positions past lens[b] are
  * never read, whatever they hold.  Several new tokens of one sequence are
  * several rows of the batch, with the same table row and growing lens.
- * Results do not depend on timing: the same call gives the same bytes. */
+ * Results do not depend on timing: the same call gives the same bytes.
+ * SPAVA_ERR_UNSUPPORTED if the tables hold 2^31 work units or more (a unit is
+ * 32 KiB of K and V rows of one KV head and 16, or 8, query heads). */
 spava_status spava_cache_attn(const spava_cache_config *cfg, const spava_cache_pools *pools,
                               const spava_cache_batch *batch, const void *q, void *o, float *lse,
                               void *ws, size_t ws_bytes, void *stream);

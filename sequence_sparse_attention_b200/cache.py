@@ -70,22 +70,39 @@ def cache_workspace_size(lay: CacheLayout) -> int:
     return n.value
 
 
-def _check(t, shape, dtype, device, name):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name}: expected contiguous {dtype} {shape} on {device}, got "
+# A decode step makes these calls many thousand times a second on tensors of a
+# few KiB, so a call's host time is most of its cost: the checks below look at
+# each property once, and outputs come from empty_like, the cheapest allocation.
+_bf16, _f32, _i32 = torch.bfloat16, torch.float32, torch.int32
+_empty_like = torch.empty_like
+
+
+def _check(t, shape, dtype, index, name):
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != index:
+        raise ValueError(f"{name}: expected contiguous {dtype} {tuple(shape)} on cuda:{index}, got "
                          f"{t.dtype} {tuple(t.shape)} on {t.device} contiguous={t.is_contiguous()}")
 
 
-def _token_stride(t, heads, d, device, name):
+def _token_stride(t, rows, heads, d, index, name):
     """Elements between the tokens of a bf16 [rows, heads, d] tensor or view."""
-    shape = t.shape
-    if t.dtype != torch.bfloat16 or len(shape) != 3 or shape[1] != heads or shape[2] != d or t.device != device:
-        raise ValueError(f"{name}: expected torch.bfloat16 (rows, {heads}, {d}) on {device}, got "
-                         f"{t.dtype} {tuple(shape)} on {t.device}")
-    stride = t.stride()
-    if stride[2] != 1 or (heads > 1 and stride[1] != d):
-        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {stride}")
-    return stride[0] if shape[0] > 1 else heads * d
+    if t.dtype != _bf16 or t.shape != (rows, heads, d) or t.get_device() != index:
+        raise ValueError(f"{name}: expected torch.bfloat16 ({rows}, {heads}, {d}) on cuda:{index}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    token, head, one = t.stride()
+    if one != 1 or (head != d and heads > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
+    return token if rows > 1 else heads * d
+
+
+def _rows(t, name):
+    if t.dim() != 3:
+        raise ValueError(f"{name}: expected (rows, heads, d), got {tuple(t.shape)}")
+    return t.shape[0]
+
+
+# The raw stream handle without a Stream object (1 us less a call), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 class _OnDevice:
@@ -97,13 +114,17 @@ class _OnDevice:
             raise ValueError(f"expected a CUDA device, got {device}")
         index = torch.cuda.current_device() if device.index is None else device.index
         self.device, self._index = torch.device("cuda", index), index
+        self._lib = native.load()
 
     def _call(self, name, *args):
-        if torch.cuda.current_device() == self._index:
-            native.call(name, *args, torch.cuda.current_stream(self._index).cuda_stream)
+        index = self._index
+        if torch.cuda.current_device() == index:
+            rc = getattr(self._lib, name)(*args, _raw_stream(index))
         else:
-            with torch.cuda.device(self._index):
-                native.call(name, *args, torch.cuda.current_stream(self._index).cuda_stream)
+            with torch.cuda.device(index):
+                rc = getattr(self._lib, name)(*args, _raw_stream(index))
+        if rc:
+            raise native.SpavaError(name, rc, self._lib.spava_last_cuda_error() if rc == 5 else 0)
 
 
 class QKNormRope(_OnDevice):
@@ -119,20 +140,24 @@ class QKNormRope(_OnDevice):
         if half:
             if inv_freq is None:
                 raise ValueError("inv_freq: a rotation needs it")
-            _check(inv_freq, (half,), torch.float32, self.device, "inv_freq")
+            _check(inv_freq, (half,), _f32, self._index, "inv_freq")
         for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
             if t is not None:
-                _check(t, (lay.d,), torch.bfloat16, self.device, name)
+                _check(t, (lay.d,), _bf16, self._index, name)
         self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight
         self._cfg = ctypes.byref(self.cfg)
+        self._axes = self.cfg.n_axes if half else 0
         self._tables = tuple(None if t is None else t.data_ptr() for t in (q_weight, k_weight, inv_freq))
 
     def _positions(self, positions, rows):
-        if not self.cfg.rope_dim:
+        axes = self._axes
+        if not axes:
             return None
-        if positions.dtype != torch.int32 or not positions.is_contiguous() or positions.device != self.device or \
-                positions.numel() != self.cfg.n_axes * rows or positions.shape[-1:] != (rows,):
-            raise ValueError(f"positions: expected contiguous torch.int32 ({self.cfg.n_axes}, {rows}) on "
+        if positions is None:
+            raise ValueError("positions: a rotation needs them")
+        if positions.dtype != _i32 or not positions.is_contiguous() or positions.get_device() != self._index or \
+                (positions.shape != (axes, rows) and (axes > 1 or positions.shape != (rows,))):
+            raise ValueError(f"positions: expected contiguous torch.int32 ({axes}, {rows}) on "
                              f"{self.device}, got {positions.dtype} {tuple(positions.shape)} on {positions.device}")
         return positions.data_ptr()
 
@@ -140,19 +165,17 @@ class QKNormRope(_OnDevice):
         """q [rows, Hq, d], k [rows, Hkv, d] (views of one projection are fine),
         positions int32 [axes, rows] -> contiguous q_out, k_out; in place with
         ``q_out=q`` and ``k_out=k`` where those are contiguous."""
-        lay, rows = self.lay, q.shape[0]
-        qs = _token_stride(q, lay.Hq, lay.d, self.device, "q")
-        ks = _token_stride(k, lay.Hkv, lay.d, self.device, "k")
-        if k.shape[0] != rows:
-            raise ValueError(f"k: expected {rows} rows, got {k.shape[0]}")
+        lay, index, rows = self.lay, self._index, _rows(q, "q")
+        qs = _token_stride(q, rows, lay.Hq, lay.d, index, "q")
+        ks = _token_stride(k, rows, lay.Hkv, lay.d, index, "k")
         if q_out is None:
-            q_out = torch.empty((rows, lay.Hq, lay.d), dtype=torch.bfloat16, device=self.device)
+            q_out = _empty_like(q, memory_format=torch.contiguous_format)
         else:
-            _check(q_out, (rows, lay.Hq, lay.d), torch.bfloat16, self.device, "q_out")
+            _check(q_out, q.shape, _bf16, index, "q_out")
         if k_out is None:
-            k_out = torch.empty((rows, lay.Hkv, lay.d), dtype=torch.bfloat16, device=self.device)
+            k_out = _empty_like(k, memory_format=torch.contiguous_format)
         else:
-            _check(k_out, (rows, lay.Hkv, lay.d), torch.bfloat16, self.device, "k_out")
+            _check(k_out, k.shape, _bf16, index, "k_out")
         self._call("spava_qk_norm_rope", self._cfg, rows, q.data_ptr(), qs, k.data_ptr(), ks, *self._tables,
                    self._positions(positions, rows), q_out.data_ptr(), k_out.data_ptr())
         return q_out, k_out
@@ -178,7 +201,7 @@ class PagedCache(_OnDevice):
             if t is None:
                 return torch.zeros(shape, dtype=torch.uint8 if dtype.itemsize == 1 else dtype,
                                    device=self.device).view(dtype)
-            _check(t, shape, dtype, self.device, name)
+            _check(t, shape, dtype, self._index, name)
             return t
 
         self.k_pages = pool(k_pages, shape, lay.dtype, "k_pages")
@@ -193,6 +216,8 @@ class PagedCache(_OnDevice):
         self._pools = SpavaCachePools(*(None if t is None else t.data_ptr()
                                         for t in (self.k_pages, self.v_pages, self.k_exp, self.v_exp)))
         self._head = (ctypes.byref(self.cfg), ctypes.byref(self._pools))
+        self._own_ws = self._check_ws(self.workspace)
+        self._lse_of = torch.empty((lay.Hq, 1), dtype=_f32, device=self.device)
 
     @property
     def tensors(self):
@@ -203,21 +228,24 @@ class PagedCache(_OnDevice):
     def new_workspace(self):
         return torch.zeros(self._ws_bytes, dtype=torch.uint8, device=self.device)
 
-    def _ws(self, workspace):
-        ws = self.workspace if workspace is None else workspace
-        if ws.dtype != torch.uint8 or ws.device != self.device or not ws.is_contiguous():
+    def _check_ws(self, ws):
+        if ws.dtype != torch.uint8 or ws.get_device() != self._index or not ws.is_contiguous():
             raise ValueError(f"workspace: expected contiguous torch.uint8 on {self.device}")
         return ws.data_ptr(), ws.numel()
 
+    def _ws(self, workspace):
+        return self._own_ws if workspace is None else self._check_ws(workspace)
+
     def _batch(self, table, lens):
-        n = lens.shape[0] if lens.dim() == 1 else -1
-        if table.dtype != torch.int32 or lens.dtype != torch.int32 or n < 0 or table.dim() != 2 or \
-                table.shape[0] != n or not table.is_contiguous() or not lens.is_contiguous() or \
-                table.device != self.device or lens.device != self.device:
-            raise ValueError(f"table, lens: expected contiguous torch.int32 (sequences, max_pages) and (sequences,) "
-                             f"on {self.device}, got {table.dtype} {tuple(table.shape)} on {table.device} and "
-                             f"{lens.dtype} {tuple(lens.shape)} on {lens.device}")
-        return n, ctypes.byref(SpavaCacheBatch(n, table.shape[1], table.data_ptr(), lens.data_ptr()))
+        if lens.dtype == _i32 and table.dtype == _i32 and lens.dim() == 1 and table.dim() == 2 and \
+                lens.is_contiguous() and table.is_contiguous() and \
+                lens.get_device() == self._index == table.get_device():
+            n, pages = table.shape
+            if lens.shape[0] == n:
+                return n, ctypes.byref(SpavaCacheBatch(n, pages, table.data_ptr(), lens.data_ptr()))
+        raise ValueError(f"table, lens: expected contiguous torch.int32 (sequences, max_pages) and (sequences,) "
+                         f"on {self.device}, got {table.dtype} {tuple(table.shape)} on {table.device} and "
+                         f"{lens.dtype} {tuple(lens.shape)} on {lens.device}")
 
     @staticmethod
     def _new_rows(rows, n, name):
@@ -229,30 +257,25 @@ class PagedCache(_OnDevice):
 
     def write(self, k, v, table, lens, workspace=None):
         """k, v [sequences * new, Hkv, d] (views fine): the last ``new`` positions of every sequence."""
-        lay, (n, batch) = self.lay, self._batch(table, lens)
-        ks = _token_stride(k, lay.Hkv, lay.d, self.device, "k")
-        vs = _token_stride(v, lay.Hkv, lay.d, self.device, "v")
-        if v.shape[0] != k.shape[0]:
-            raise ValueError(f"v: expected {k.shape[0]} rows, got {v.shape[0]}")
-        self._call("spava_cache_write", *self._head, batch, self._new_rows(k.shape[0], n, "k"), k.data_ptr(), ks,
+        lay, index, (n, batch), rows = self.lay, self._index, self._batch(table, lens), _rows(k, "k")
+        ks = _token_stride(k, rows, lay.Hkv, lay.d, index, "k")
+        vs = _token_stride(v, rows, lay.Hkv, lay.d, index, "v")
+        self._call("spava_cache_write", *self._head, batch, self._new_rows(rows, n, "k"), k.data_ptr(), ks,
                    v.data_ptr(), vs, *self._ws(workspace))
 
     def append(self, rope: QKNormRope, q, k, v, positions, table, lens, q_out=None, workspace=None):
         """``rope.apply(q, k, positions)`` and ``write`` of its keys and of v, in one
         launch; returns the queries.  ``positions`` are the rotation's, [axes, sequences * new]."""
-        lay, (n, batch) = self.lay, self._batch(table, lens)
-        rows = q.shape[0]
-        if rope.device != self.device:
+        lay, index, (n, batch), rows = self.lay, self._index, self._batch(table, lens), _rows(q, "q")
+        if rope._index != index:
             raise ValueError(f"rope: expected on {self.device}, is on {rope.device}")
-        qs = _token_stride(q, lay.Hq, lay.d, self.device, "q")
-        ks = _token_stride(k, lay.Hkv, lay.d, self.device, "k")
-        vs = _token_stride(v, lay.Hkv, lay.d, self.device, "v")
-        if k.shape[0] != rows or v.shape[0] != rows:
-            raise ValueError(f"k, v: expected {rows} rows, got {k.shape[0]} and {v.shape[0]}")
+        qs = _token_stride(q, rows, lay.Hq, lay.d, index, "q")
+        ks = _token_stride(k, rows, lay.Hkv, lay.d, index, "k")
+        vs = _token_stride(v, rows, lay.Hkv, lay.d, index, "v")
         if q_out is None:
-            q_out = torch.empty((rows, lay.Hq, lay.d), dtype=torch.bfloat16, device=self.device)
+            q_out = _empty_like(q, memory_format=torch.contiguous_format)
         else:
-            _check(q_out, (rows, lay.Hq, lay.d), torch.bfloat16, self.device, "q_out")
+            _check(q_out, q.shape, _bf16, index, "q_out")
         self._call("spava_cache_append", rope._cfg, *self._head, batch, self._new_rows(rows, n, "q"),
                    q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, *rope._tables,
                    rope._positions(positions, rows), q_out.data_ptr(), *self._ws(workspace))
@@ -262,31 +285,36 @@ class PagedCache(_OnDevice):
         """Positions [first, first + rows) of every sequence as bf16 [sequences, rows,
         Hkv, d], keys and values; zeros from position lens[b] on."""
         lay, (n, batch) = self.lay, self._batch(table, lens)
-        shape, out = (n, rows, lay.Hkv, lay.d), []
-        for t, name in ((k_out, "k_out"), (v_out, "v_out")):
-            if t is None:
-                t = torch.empty(shape, dtype=torch.bfloat16, device=self.device)
-            else:
-                _check(t, shape, torch.bfloat16, self.device, name)
-            out.append(t)
-        self._call("spava_cache_read", *self._head, batch, first, rows, out[0].data_ptr(), out[1].data_ptr(),
+        shape = (n, rows, lay.Hkv, lay.d)
+        if k_out is None:
+            k_out = torch.empty(shape, dtype=_bf16, device=self.device)
+        else:
+            _check(k_out, shape, _bf16, self._index, "k_out")
+        if v_out is None:
+            v_out = _empty_like(k_out)
+        else:
+            _check(v_out, shape, _bf16, self._index, "v_out")
+        self._call("spava_cache_read", *self._head, batch, first, rows, k_out.data_ptr(), v_out.data_ptr(),
                    *self._ws(workspace))
-        return tuple(out)
+        return k_out, v_out
 
     def attn(self, q, table, lens, o=None, lse=None, want_lse=True, workspace=None):
         """One query token per sequence, q [sequences, Hq, d], over positions [0,
         lens[b]): o like q, and lse float32 [Hq, sequences] (natural log; -inf and
         o = 0 for a sequence without positions)."""
         lay, (n, batch) = self.lay, self._batch(table, lens)
-        _check(q, (n, lay.Hq, lay.d), torch.bfloat16, self.device, "q")
+        _check(q, (n, lay.Hq, lay.d), _bf16, self._index, "q")
         if o is None:
-            o = torch.empty_like(q)
+            o = _empty_like(q)
         else:
-            _check(o, (n, lay.Hq, lay.d), torch.bfloat16, self.device, "o")
+            _check(o, q.shape, _bf16, self._index, "o")
         if lse is not None:
-            _check(lse, (lay.Hq, n), torch.float32, self.device, "lse")
+            _check(lse, (lay.Hq, n), _f32, self._index, "lse")
         elif want_lse:
-            lse = torch.empty((lay.Hq, n), dtype=torch.float32, device=self.device)
+            like = self._lse_of  # of the last batch size; a local, as other threads may change it
+            if like.shape[1] != n:
+                self._lse_of = like = torch.empty((lay.Hq, n), dtype=_f32, device=self.device)
+            lse = _empty_like(like)
         self._call("spava_cache_attn", *self._head, batch, q.data_ptr(), o.data_ptr(),
                    None if lse is None else lse.data_ptr(), *self._ws(workspace))
         return o, lse

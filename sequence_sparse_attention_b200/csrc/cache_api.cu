@@ -78,10 +78,13 @@ spava_status make_view(const spava_cache_config *c, const spava_cache_pools *p,
     if (!p || !b) return SPAVA_ERR_INVALID_ARG;
     if (b->n_seqs < 0 || b->max_pages < 1) return SPAVA_ERR_INVALID_ARG;
     if (b->n_seqs >= (1LL << 20)) return SPAVA_ERR_UNSUPPORTED;
-    if (b->max_pages >= ((1LL << 31) + c->page_size - 1) / c->page_size) return SPAVA_ERR_UNSUPPORTED;
+    if (b->max_pages > ((1LL << 31) - 65536) / c->page_size) return SPAVA_ERR_UNSUPPORTED;
     SPAVA_TRY(check_ptr(p->k));
     SPAVA_TRY(check_ptr(p->v));
-    if (c->type == SPAVA_CACHE_E4M3 && (!p->k_exp || !p->v_exp)) return SPAVA_ERR_INVALID_ARG;
+    if (c->type == SPAVA_CACHE_E4M3) {
+        SPAVA_TRY(check_ptr(p->k_exp));
+        SPAVA_TRY(check_ptr(p->v_exp));
+    }
     if (!b->table || !b->lens) return SPAVA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(b->table) & 3) || (reinterpret_cast<uintptr_t>(b->lens) & 3))
         return SPAVA_ERR_MISALIGNED;
@@ -97,6 +100,7 @@ spava_status make_view(const spava_cache_config *c, const spava_cache_pools *p,
     v->status = static_cast<int *>(ws);
     v->max_pages = b->max_pages;
     v->n_pages = static_cast<uint32_t>(std::min<int64_t>(c->n_pages, INT32_MAX));
+    v->n_rows = static_cast<uint32_t>(c->n_pages * c->n_kv_heads * c->page_size);
     v->n_seqs = static_cast<int32_t>(b->n_seqs);
     v->Hkv = c->n_kv_heads;
     v->cap = static_cast<int32_t>(b->max_pages * c->page_size);
@@ -328,6 +332,10 @@ spava_status spava_cache_attn(const spava_cache_config *cfg, const spava_cache_p
     p.part_o = p.part_stat + size_t(2) * kDecMaxCtas * 3 * 8 * nt;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool e4m3 = cfg->type == SPAVA_CACHE_E4M3;
+    // the units of a batch of full tables are counted in 32 bits
+    const int64_t block = int64_t(kDecWarps) * kDecTileBytes / (2 * cfg->head_dim * (e4m3 ? 1 : 2));
+    const int64_t units = (p.cache.cap + block - 1) / block * cfg->n_kv_heads * p.n_hg;
+    if (units >= (1LL << 31) / batch->n_seqs) return SPAVA_ERR_UNSUPPORTED;
     if (cfg->head_dim == 64) {
         if (e4m3) return nt == 1 ? launch_decode<64, true, 1>(p, st) : launch_decode<64, true, 2>(p, st);
         return nt == 1 ? launch_decode<64, false, 1>(p, st) : launch_decode<64, false, 2>(p, st);

@@ -45,7 +45,7 @@ struct CacheView {
     const int32_t *lens;
     int *status;
     int64_t max_pages;
-    uint32_t n_pages;
+    uint32_t n_pages, n_rows;  // of the pool; n_rows = n_pages * Hkv * page_size
     int32_t n_seqs, Hkv;
     int32_t cap;  // positions of the table: max_pages * page_size
     FastDiv page;

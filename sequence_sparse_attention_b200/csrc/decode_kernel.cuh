@@ -12,6 +12,7 @@ constexpr int kDecMaxCtas = 320;  // the workspace's partials are sized for thes
 constexpr int kDecStages = 3;
 constexpr int kDecTileBytes = 8192;  // K and V bytes of one warp's tile
 constexpr int kDecRingBytes = kDecWarps * kDecStages * kDecTileBytes;
+constexpr int kDecPageSlots = kDecStages + 1;  // tiles whose table entries are under way
 
 struct DecodeParams {
     CacheView cache;
@@ -31,8 +32,8 @@ __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32
                  "r"(bytes)
                  : "memory");
 }
-__device__ __forceinline__ void cp_async8(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, uint32_t bytes) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(bytes)
                  : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -52,6 +53,14 @@ __device__ __forceinline__ uint2 lds8(uint32_t a) {
     uint2 r;
     asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a) : "memory");
     return r;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t a) {
+    uint32_t r;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(r) : "r"(a) : "memory");
+    return r;
+}
+__device__ __forceinline__ void sts4(uint32_t a, uint32_t v) {
+    asm volatile("st.shared.u32 [%0], %1;" ::"r"(a), "r"(v) : "memory");
 }
 template <bool HALF>
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -93,18 +102,34 @@ struct DecodeShape {
     static constexpr int TT = kDecTileBytes / (2 * ROW);   // tokens of a warp's tile
     static constexpr int SUB = TT / 16;                    // MMA tiles of 16 tokens
     static constexpr int BLOCK = TT * kDecWarps;           // tokens of a work unit
+    static constexpr int LPR = ROW / 16;                   // lanes that copy a row
+    static constexpr int RPI = 32 / LPR;                   // rows that a copy instruction of the warp takes
     static constexpr int KJ = ROW / 64;                    // 16-byte pieces of a K row per lane
     static constexpr int VB = ROW / 8;                     // bytes of a V row per lane
     static constexpr int KS = D / 16;                      // k steps of a score
     static constexpr int MT = D / 16;                      // 16-row tiles of O^T
     static constexpr int HEADS = 8 * NT;
+    // The 16-byte pieces of a row lie permuted (piece ^ swizzle) so that the
+    // eight lanes that read at a time, pieces c of the K rows g, g + 1 or pieces
+    // g, g + 1 of the V rows 2c, meet all banks.
+    __host__ __device__ static constexpr int k_swizzle(int row) { return ROW >= 128 ? (row & 1) * 4 : 0; }
+    __host__ __device__ static constexpr int v_swizzle(int row) {
+        return ROW >= 128 ? (row >> 1 & 3) * 2 : row >> 1 & 3;
+    }
     static constexpr int OPAD = D + 4;                     // floats of an O row in shared memory
     // The ring is free when a segment is joined, and takes the warps' O and
     // statistics, then the join's weights.
     static constexpr int MERGE = kDecWarps * HEADS * (OPAD + 3) * 4 + HEADS * 2 * 4;
-    static constexpr int JOIN = HEADS * (kDecMaxCtas + 3) * 4;
+    static constexpr int ROWS4 = HEADS * D / 128;          // float4s of a partial O per lane of a warp
+    // the join: every part's statistics, the results' statistics, the warps' sums
+    static constexpr int JOIN = (HEADS * (kDecMaxCtas * 3 + 3) + kDecWarps * HEADS * D) * 4;
     static constexpr int A = MERGE > kDecRingBytes ? MERGE : kDecRingBytes;
-    static constexpr int SMEM = A > JOIN ? A : JOIN;
+    static constexpr int RING = A > JOIN ? A : JOIN;
+    // behind it: table entries and, of an e4m3 cache, the words with the rows' exponents
+    static constexpr int RW = TT == 64 ? 2 : 1;            // tokens of a tile per lane
+    static constexpr int PAGES = kDecPageSlots * RW * 128;         // bytes, a warp
+    static constexpr int EXPS = E4M3 ? kDecStages * RW * 2 * 128 : 0;
+    static constexpr int SMEM = RING + kDecWarps * (PAGES + EXPS);
 };
 
 // What bounds it: every cached row is read once, D bytes or 2 D, and takes
@@ -112,12 +137,14 @@ struct DecodeShape {
 // cores do per byte of HBM, so the kernel is a read of the cache with
 // arithmetic beside it, and all choices keep that read running:
 //
-//   - Every lane copies with cp.async just the bytes that it will itself feed
-//     to the matrix instructions, into a ring of its own, and only ever waits
-//     for its own copies: no barrier in the loop, no address constraint but 16
-//     bytes, so pages may have any size and end inside a tile.  The
-//     contraction order over d is free, so a lane takes 16 contiguous bytes of
-//     a K row for two to four k steps; O's rows are permuted likewise for V.
+//   - Every warp copies its own tiles with cp.async, row by row, into a ring of
+//     its own: no block barrier in the loop, no address constraint but 16
+//     bytes, so pages may have any size and end inside a tile.  Each copy
+//     instruction takes 512 contiguous bytes where rows follow each other
+//     (measured, 268 MB: 42 us; lanes that copy just what they will read
+//     themselves, V rows at 512 bytes' stride: 58 us).  The contraction order
+//     over d is free, so a lane reads 16 contiguous bytes of a K row for two to
+//     four k steps; O's rows are permuted likewise for V.
 //   - Transposed products, S^T = K Q^T and O^T = V^T P^T: tokens (or d) take
 //     the 16-row side of an MMA and the query heads the 8-column side, so G = 7
 //     or 4 wastes little, and the accumulators are 4 NT D / 16 registers.
@@ -141,8 +168,8 @@ template <int D, bool E4M3, int NT>
 __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_constant__ DecodeParams p) {
     using S = DecodeShape<D, E4M3, NT>;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int64_t s_prefix[kDecThreads + 1];
-    __shared__ int64_t s_warp[kDecWarps];
+    __shared__ int s_prefix[kDecThreads + 1];
+    __shared__ int s_warp[kDecWarps];
     __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int g = lane / 4, c = lane % 4;
@@ -151,13 +178,12 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
 
     // ---- the line of units: thread t holds the sequences [t * per, (t+1) * per)
     const int per = (cv.n_seqs + kDecThreads - 1) / kDecThreads;
-    int64_t mine = 0;
+    int scan = 0;
     for (int b = tid * per; b < min((tid + 1) * per, cv.n_seqs); ++b)
-        mine += (cache_len(cv, b) + S::BLOCK - 1) / S::BLOCK;
-    int64_t scan = mine;
+        scan += (cache_len(cv, b) + S::BLOCK - 1) / S::BLOCK;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, scan, o);
+        const int x = __shfl_up_sync(0xffffffffu, scan, o);
         if (lane >= o) scan += x;
     }
     if (lane == 31) s_warp[warp] = scan;
@@ -168,7 +194,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
     s_prefix[tid + 1] = scan * per_seq;
     if (tid == 0) s_prefix[0] = 0;
     __syncthreads();
-    const int64_t total = s_prefix[kDecThreads];
+    const int total = s_prefix[kDecThreads];
 
     // ---- sequences without positions
     for (int b = blockIdx.x; b < cv.n_seqs; b += gridDim.x) {
@@ -180,14 +206,20 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
                 p.lse[static_cast<int64_t>(h) * cv.n_seqs + b] = -INFINITY;
     }
 
-    const int64_t ctas = total < gridDim.x ? total : gridDim.x;  // blocks with a share
-    if (blockIdx.x >= ctas) return;
-    int64_t u = blockIdx.x * total / ctas;
-    const int64_t u_end = (blockIdx.x + 1) * total / ctas;
+    // Shares of `base` units, of one more for the first `more` blocks.
+    const int ctas = min(total, static_cast<int>(gridDim.x));  // blocks with a share
+    const int cta = blockIdx.x;
+    if (cta >= ctas) return;
+    const int base = total / ctas, more = total - base * ctas;
+    int u = cta * base + min(cta, more);
+    const int u_end = u + base + (cta < more ? 1 : 0);
+    auto cta_of = [&](int x) {
+        const int y = x - more * (base + 1);
+        return y < 0 ? x / (base + 1) : more + y / base;
+    };
 
     // ---- the sequence of the first unit
-    int b;
-    int64_t first;  // unit where sequence b begins
+    int b, first;  // first: the unit where sequence b begins
     {
         int lo = 0, hi = kDecThreads;  // s_prefix[lo] <= u < s_prefix[hi]
         while (hi - lo > 1) {
@@ -200,20 +232,22 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
     int len = cache_len(cv, b);
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) +
                           warp * (kDecStages * kDecTileBytes);
+    const uint32_t side = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + S::RING +
+                          warp * (S::PAGES + S::EXPS) + lane * 4;
 
     while (u < u_end) {
-        int64_t blocks = (len + S::BLOCK - 1) / S::BLOCK;
+        int blocks = (len + S::BLOCK - 1) / S::BLOCK;
         while (u >= first + blocks * per_seq) {
             first += blocks * per_seq;
             len = cache_len(cv, ++b);
             blocks = (len + S::BLOCK - 1) / S::BLOCK;
         }
-        const int item = static_cast<int>((u - first) / blocks);
-        const int64_t item_u0 = first + item * blocks, item_u1 = item_u0 + blocks;
+        const int item = (u - first) / blocks;
+        const int item_u0 = first + item * blocks, item_u1 = item_u0 + blocks;
         const int kvh = item / p.n_hg, hg = item - kvh * p.n_hg;
-        const int64_t seg_end = u_end < item_u1 ? u_end : item_u1;
-        const int n = static_cast<int>(seg_end - u);                      // tiles of this warp
-        const int t0 = static_cast<int>(u - item_u0) * S::BLOCK + warp * S::TT;  // first token of tile 0
+        const int seg_end = min(u_end, item_u1);
+        const int n = seg_end - u;                           // tiles of this warp
+        const int t0 = (u - item_u0) * S::BLOCK + warp * S::TT;  // first token of tile 0
         const int head0 = kvh * p.G + hg * S::HEADS;
         const int n_heads = min(S::HEADS, p.G - hg * S::HEADS);
         const uint32_t head_rows = static_cast<uint32_t>(kvh) * cv.page.d;
@@ -277,92 +311,108 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
         }
 
         // ---- the ring
-        // Lane i looks up the pool rows of the tokens i, i + 32 of a tile (of
-        // i % 16 where a tile has 16).
-        constexpr int RW = S::TT == 64 ? 2 : 1;
-        auto look_up = [&](int i, uint32_t (&r)[RW]) {
-#pragma unroll
-            for (int k = 0; k < RW; ++k) {
-                const int64_t t = static_cast<int64_t>(t0) + static_cast<int64_t>(i) * S::BLOCK +
-                                  (S::TT == 16 ? lane % 16 : lane + 32 * k);
-                r[k] = kNoRow;
-                if (i < n && t < len) {
-                    r[k] = cache_row(cv, b, static_cast<int>(t));
-                    if (r[k] != kNoRow) r[k] += head_rows;
-                }
+        // Lane i takes care of the tokens i, i + 32 of a tile (i % 16 where a tile
+        // has 16): their table entries come by cp.async too, K tiles before the
+        // rows that they lead to are asked for, as a load that a register waits
+        // for would hold up the warp (measured: 58 instead of 43 us for a stream
+        // of 268 MB).
+        constexpr int RW = S::RW, K = kDecStages - 1;
+        const int32_t *table = cv.table + b * cv.max_pages;
+        auto token = [&](int i, int k) {
+            return static_cast<int64_t>(t0) + static_cast<int64_t>(i) * S::BLOCK +
+                   (S::TT == 16 ? lane % 16 : lane + 32 * k);
+        };
+        auto held_token = [&](int i, int64_t t) { return i < n && t < len; };
+        auto row_of = [&](int i, int k, int page) {  // pool row of this lane's k-th token of tile i
+            const int64_t t = token(i, k);
+            if (!held_token(i, t)) return kNoRow;
+            if (static_cast<uint32_t>(page) >= cv.n_pages) {
+                atomicOr(cv.status, kStatusBadBatch);
+                return kNoRow;
             }
+            uint32_t off;
+            cv.page.quot(static_cast<uint32_t>(t), off);
+            return static_cast<uint32_t>(page) * cv.Hkv * cv.page.d + head_rows + off;
         };
         auto issue = [&](int stage, const uint32_t (&r)[RW]) {
+            if (E4M3) {
+                // the aligned word with the row's exponent; its end may lie behind the pool's
+#pragma unroll
+                for (int k = 0; k < RW; ++k) {
+                    const uint32_t at = r[k] & ~3u, to = side + S::PAGES + (stage * RW + k) * 256;
+                    const uint32_t bytes = r[k] == kNoRow ? 0 : min(4u, cv.n_rows - at);
+                    cp_async4(to, cv.k_exp + (bytes ? at : 0), bytes);
+                    cp_async4(to + 128, cv.v_exp + (bytes ? at : 0), bytes);
+                }
+            }
             const uint32_t dst = ring + stage * kDecTileBytes;
-            const char *kp = static_cast<const char *>(cv.k), *vp = static_cast<const char *>(cv.v);
+            const int piece = lane % S::LPR;
 #pragma unroll
-            for (int s = 0; s < S::SUB; ++s) {
-                const uint32_t rs = r[S::TT == 64 ? s / 2 : 0];
-                const int from = S::TT == 16 ? 0 : (s % 2) * 16;
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                    const uint32_t row = __shfl_sync(0xffffffffu, rs, from + g + 8 * y);
-                    const char *src = kp + (row == kNoRow ? 0 : static_cast<int64_t>(row) * S::ROW) + c * 16;
-#pragma unroll
-                    for (int j = 0; j < S::KJ; ++j)
-                        cp_async16(dst + ((s * 2 + y) * S::KJ + j) * 512 + lane * 16, src + j * 64,
-                                   row == kNoRow ? 0 : 16);
-                }
-                const uint32_t vdst = dst + kDecTileBytes / 2 + s * 16 * S::ROW;
-#pragma unroll
-                for (int y = 0; y < 4; ++y) {
-                    const uint32_t row = __shfl_sync(0xffffffffu, rs, from + 2 * c + (y & 1) + 8 * (y >> 1));
-                    const char *src = vp + (row == kNoRow ? 0 : static_cast<int64_t>(row) * S::ROW);
-                    if (S::VB == 8) {
-                        cp_async8(vdst + y * 256 + lane * 8, src + g * 8, row == kNoRow ? 0 : 8);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < S::VB / 16; ++j)
-                            cp_async16(vdst + (y * (S::VB / 16) + j) * 512 + lane * 16,
-                                       src + g * 16 + j * 128, row == kNoRow ? 0 : 16);
-                    }
-                }
+            for (int x = 0; x < 8; ++x) {
+                const int at = x * S::RPI + lane / S::LPR;  // row of the tile
+                const uint32_t row = __shfl_sync(0xffffffffu, r[x * S::RPI / 32], at % 32);
+                const int64_t from = row == kNoRow ? 0 : static_cast<int64_t>(row) * S::ROW + piece * 16;
+                const uint32_t bytes = row == kNoRow ? 0 : 16;
+                cp_async16(dst + at * S::ROW + (piece ^ S::k_swizzle(at)) * 16,
+                           static_cast<const char *>(cv.k) + from, bytes);
+                cp_async16(dst + kDecTileBytes / 2 + at * S::ROW + (piece ^ S::v_swizzle(at)) * 16,
+                           static_cast<const char *>(cv.v) + from, bytes);
             }
         };
-        auto load_exps = [&](const uint32_t (&r)[RW], int (&ke)[RW], int (&ve)[RW]) {
-#pragma unroll
-            for (int k = 0; k < RW; ++k) {
-                ke[k] = ve[k] = 0;
-                if (E4M3 && r[k] != kNoRow) {
-                    ke[k] = __ldg(cv.k_exp + r[k]);
-                    ve[k] = __ldg(cv.v_exp + r[k]);
-                }
-            }
-        };
-
         uint32_t rows[kDecStages][RW];  // of the tiles i, i + 1, ... in flight
+        {
+            int page[2 * K + 1][RW];  // of the tiles 0 ... 2 K
 #pragma unroll
-        for (int i = 0; i < kDecStages; ++i) look_up(i, rows[i]);
-        int ke[RW], ve[RW];
-        load_exps(rows[0], ke, ve);
+            for (int i = 0; i <= 2 * K; ++i)
 #pragma unroll
-        for (int i = 0; i < kDecStages - 1; ++i) {
-            issue(i, rows[i]);
-            cp_async_commit();
-        }
-
-        int stage = 0;
-        for (int i = 0; i < n; ++i) {
-            {
-                const int to = stage == 0 ? kDecStages - 1 : stage - 1;
-                if (i + kDecStages - 1 < n) issue(to, rows[kDecStages - 1]);
+                for (int k = 0; k < RW; ++k) {
+                    const int64_t t = token(i, k);
+                    page[i][k] = held_token(i, t) ? __ldg(table + cv.page.quot(static_cast<uint32_t>(t))) : 0;
+                }
+#pragma unroll
+            for (int i = 0; i < K; ++i) {
+#pragma unroll
+                for (int k = 0; k < RW; ++k) rows[i][k] = row_of(i, k, page[i][k]);
+                issue(i, rows[i]);
                 cp_async_commit();
             }
-            uint32_t ahead[RW];
-            look_up(i + kDecStages, ahead);
-            int ke_next[RW], ve_next[RW];
-            load_exps(rows[1], ke_next, ve_next);
-            cp_async_wait<kDecStages - 1>();
+#pragma unroll
+            for (int i = K; i <= 2 * K; ++i)
+#pragma unroll
+                for (int k = 0; k < RW; ++k) sts4(side + ((i % kDecPageSlots) * RW + k) * 128, page[i][k]);
+        }
+
+        int stage = 0, slot = K % kDecPageSlots;  // slot: of tile i + K's table entries
+        for (int i = 0; i < n; ++i) {
+            // group i + K: the rows of tile i + K, the table entries of tile i + 2 K + 1
+#pragma unroll
+            for (int k = 0; k < RW; ++k)
+                rows[K][k] = row_of(i + K, k, static_cast<int>(lds4(side + (slot * RW + k) * 128)));
+            __syncwarp();  // every lane has read what the new copies replace
+            if (i + K < n) issue(stage == 0 ? K : stage - 1, rows[K]);
+            {
+                const int to = slot == 0 ? kDecPageSlots - 1 : slot - 1;  // (i + 2 K + 1) % slots
+#pragma unroll
+                for (int k = 0; k < RW; ++k) {
+                    const int64_t t = token(i + 2 * K + 1, k);
+                    if (held_token(i + 2 * K + 1, t))
+                        cp_async4(side + (to * RW + k) * 128, table + cv.page.quot(static_cast<uint32_t>(t)), 4);
+                }
+            }
+            cp_async_commit();
+            slot = slot == kDecPageSlots - 1 ? 0 : slot + 1;
+            cp_async_wait<K>();
+            __syncwarp();
 
             // ---- scores of TT tokens, s[...][x]: token g (x < 2) or g + 8, head 2c + x % 2
             const uint32_t src = ring + stage * kDecTileBytes;
+            const uint32_t ksrc = src + g * S::ROW, vsrc0 = src + kDecTileBytes / 2 + 2 * c * S::ROW;
             float s[S::SUB][NT][4];
             float v_exp[S::SUB][2];
+            auto exp_of = [&](int which, int k) {  // 0: of K, 128: of V; this lane's k-th token
+                const uint32_t w = lds4(side + S::PAGES + (stage * RW + k) * 256 + which);
+                return static_cast<int>(static_cast<int8_t>(w >> (8 * (rows[0][k] & 3))));
+            };
             uint32_t held[RW];
 #pragma unroll
             for (int k = 0; k < RW; ++k) held[k] = __ballot_sync(0xffffffffu, rows[0][k] != kNoRow);
@@ -375,8 +425,9 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
                     for (int k = 0; k < 4; ++k) s[sb][t][k] = 0.f;
 #pragma unroll
                 for (int j = 0; j < S::KJ; ++j) {
-                    const uint4 a = lds16(src + (sb * 2 * S::KJ + j) * 512 + lane * 16);
-                    const uint4 e = lds16(src + ((sb * 2 + 1) * S::KJ + j) * 512 + lane * 16);
+                    const int piece = ((c + 4 * j) ^ S::k_swizzle(g)) * 16;
+                    const uint4 a = lds16(ksrc + sb * 16 * S::ROW + piece);
+                    const uint4 e = lds16(ksrc + (sb * 16 + 8) * S::ROW + piece);
                     if (!E4M3) {
 #pragma unroll
                         for (int t = 0; t < NT; ++t) {
@@ -404,11 +455,11 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
                 float kf[2] = {1.f, 1.f};
                 v_exp[sb][0] = v_exp[sb][1] = 0.f;
                 if (E4M3) {
+                    const int ke = exp_of(0, two ? sb / 2 : 0), ve = exp_of(128, two ? sb / 2 : 0);
 #pragma unroll
                     for (int y = 0; y < 2; ++y) {
-                        kf[y] = pow2f(max(__shfl_sync(0xffffffffu, ke[two ? sb / 2 : 0], from + g + 8 * y), -126));
-                        v_exp[sb][y] = static_cast<float>(
-                            __shfl_sync(0xffffffffu, ve[two ? sb / 2 : 0], from + g + 8 * y));
+                        kf[y] = pow2f(max(__shfl_sync(0xffffffffu, ke, from + g + 8 * y), -126));
+                        v_exp[sb][y] = static_cast<float>(__shfl_sync(0xffffffffu, ve, from + g + 8 * y));
                     }
                 }
                 const uint32_t bits = held[two ? sb / 2 : 0] >> from;
@@ -477,13 +528,13 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
                             lo[t][y] = movmatrix_trans(bf_pack(w[0] - bf_lo(h), w[1] - bf_hi(h)));
                         }
                     }
-                const uint32_t vsrc = src + kDecTileBytes / 2 + sb * 16 * S::ROW;
+                const uint32_t vsrc = vsrc0 + sb * 16 * S::ROW;  // rows 2c, 2c + 1, 2c + 8, 2c + 9 of it
                 if (!E4M3) {
 #pragma unroll
                     for (int j = 0; j < S::VB / 16; ++j) {
                         uint4 v[4];
 #pragma unroll
-                        for (int y = 0; y < 4; ++y) v[y] = lds16(vsrc + (y * (S::VB / 16) + j) * 512 + lane * 16);
+                        for (int y = 0; y < 4; ++y) v[y] = lds16(vsrc + ((y & 1) + 8 * (y >> 1)) * S::ROW + ((g + 8 * j) ^ S::v_swizzle(2 * c)) * 16);
                         const uint32_t r0[4] = {v[0].x, v[0].y, v[0].z, v[0].w};
                         const uint32_t r1[4] = {v[1].x, v[1].y, v[1].z, v[1].w};
                         const uint32_t r2[4] = {v[2].x, v[2].y, v[2].z, v[2].w};
@@ -506,11 +557,12 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
                     uint32_t v[4][W];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
+                        const uint32_t at = vsrc + ((y & 1) + 8 * (y >> 1)) * S::ROW;
                         if (S::VB == 8) {
-                            const uint2 x = lds8(vsrc + y * 256 + lane * 8);
+                            const uint2 x = lds8(at + ((g / 2) ^ S::v_swizzle(2 * c)) * 16 + g % 2 * 8);
                             v[y][0] = x.x, v[y][1] = x.y;
                         } else {
-                            const uint4 x = lds16(vsrc + y * 512 + lane * 16);
+                            const uint4 x = lds16(at + (g ^ S::v_swizzle(2 * c)) * 16);
                             v[y][0] = x.x, v[y][1] = x.y, v[y][W - 2] = x.z, v[y][W - 1] = x.w;
                         }
                     }
@@ -540,12 +592,6 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
             for (int k = 0; k < kDecStages - 1; ++k)
 #pragma unroll
                 for (int r = 0; r < RW; ++r) rows[k][r] = rows[k + 1][r];
-#pragma unroll
-            for (int r = 0; r < RW; ++r) {
-                rows[kDecStages - 1][r] = ahead[r];
-                ke[r] = ke_next[r];
-                ve[r] = ve_next[r];
-            }
             stage = stage == kDecStages - 1 ? 0 : stage + 1;
         }
         cp_async_wait<0>();
@@ -575,8 +621,8 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
                 }
             }
         __syncthreads();
-        const bool whole = u <= item_u0 && seg_end == item_u1;
-        const int slot = 2 * blockIdx.x + (u == item_u0 ? 1 : 0);
+        const bool whole = u == item_u0 && seg_end == item_u1;
+        const int part = 2 * cta + (u == item_u0 ? 1 : 0);
         // thread: one head of 4 floats of d at a time
         for (int x = tid; x < S::HEADS * D / 4; x += kDecThreads) {
             const int h = x / (D / 4), d = x % (D / 4) * 4;
@@ -599,10 +645,10 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
             }
             if (!whole) {
                 if (d == 0) {
-                    float *st = p.part_stat + static_cast<int64_t>(slot) * 3 * S::HEADS + h;
+                    float *st = p.part_stat + static_cast<int64_t>(part) * 3 * S::HEADS + h;
                     st[0] = m, st[S::HEADS] = lm, st[2 * S::HEADS] = l;
                 }
-                reinterpret_cast<float4 *>(p.part_o + (static_cast<int64_t>(slot) * S::HEADS + h) * D + d)[0] = o;
+                reinterpret_cast<float4 *>(p.part_o + (static_cast<int64_t>(part) * S::HEADS + h) * D + d)[0] = o;
             } else if (h < n_heads) {
                 const float f = l == 0.f ? 0.f : exp2f(m - lm) / l;
                 *reinterpret_cast<uint2 *>(p.o + (static_cast<int64_t>(b) * p.Hq + head0 + h) * D + d) =
@@ -615,54 +661,78 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
 
         // ---- join the blocks of a cut item: the last to arrive does it
         if (!whole) {
-            // block of unit x: the largest i with i * total / ctas <= x
-            const int c0 = static_cast<int>(((item_u0 + 1) * ctas - 1) / total);
-            const int c1 = static_cast<int>((item_u1 * ctas - 1) / total);
+            const int c0 = cta_of(item_u0), parts = cta_of(item_u1 - 1) - c0 + 1;
             __threadfence();
             __syncthreads();
             if (tid == 0) {
-                s_last = atomicAdd(p.counters + c0, 1) == c1 - c0;
+                s_last = atomicAdd(p.counters + c0, 1) == parts - 1;
                 __threadfence();
             }
             __syncthreads();
             if (s_last) {
-                const int parts = c1 - c0 + 1;
-                float *wt = reinterpret_cast<float *>(smem);      // [HEADS][kDecMaxCtas] weights
-                float *res = wt + S::HEADS * kDecMaxCtas;         // [3][HEADS]: m, lm, l
+                float *st = reinterpret_cast<float *>(smem);          // [parts][3][HEADS]: m (then O's weight), lm, l
+                float *res = st + 3 * S::HEADS * kDecMaxCtas;         // [3][HEADS]
+                float *sum = res + 3 * S::HEADS;                      // [warps][HEADS][D]
+                // part 0 is the second one of block c0, the others the first of theirs
                 auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
+                for (int x = tid; x < parts * 3 * S::HEADS; x += kDecThreads) {
+                    const int i = x / (3 * S::HEADS);
+                    st[x] = __ldcg(p.part_stat + slot_of(i) * 3 * S::HEADS + (x - i * 3 * S::HEADS));
+                }
+                __syncthreads();
                 for (int h = warp; h < S::HEADS; h += kDecWarps) {
-                    float m = kDecNone, lm = kDecNone;
+                    float m = kDecNone, lm = kDecNone, l = 0.f;
                     for (int i = lane; i < parts; i += 32) {
-                        const float *st = p.part_stat + static_cast<int64_t>(slot_of(i)) * 3 * S::HEADS + h;
-                        m = fmaxf(m, __ldcg(st));
-                        lm = fmaxf(lm, __ldcg(st + S::HEADS));
+                        m = fmaxf(m, st[i * 3 * S::HEADS + h]);
+                        lm = fmaxf(lm, st[(i * 3 + 1) * S::HEADS + h]);
                     }
 #pragma unroll
                     for (int o = 16; o; o >>= 1) {
                         m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
                         lm = fmaxf(lm, __shfl_xor_sync(0xffffffffu, lm, o));
                     }
-                    float l = 0.f;
                     for (int i = lane; i < parts; i += 32) {
-                        const float *st = p.part_stat + static_cast<int64_t>(slot_of(i)) * 3 * S::HEADS + h;
-                        wt[h * kDecMaxCtas + i] = exp2_approx(__ldcg(st) - m);
-                        l = fmaf(__ldcg(st + 2 * S::HEADS), exp2_approx(__ldcg(st + S::HEADS) - lm), l);
+                        st[i * 3 * S::HEADS + h] = exp2_approx(st[i * 3 * S::HEADS + h] - m);
+                        l = fmaf(st[(i * 3 + 2) * S::HEADS + h],
+                                 exp2_approx(st[(i * 3 + 1) * S::HEADS + h] - lm), l);
                     }
 #pragma unroll
                     for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
                     if (lane == 0) res[h] = m, res[S::HEADS + h] = lm, res[2 * S::HEADS + h] = l;
                 }
                 __syncthreads();
-                for (int x = tid; x < n_heads * D / 4; x += kDecThreads) {
+                // Warp w sums every fourth part, all rows of a part in flight at
+                // once; then the warps' sums, in order.
+                float4 o4[S::ROWS4];
+#pragma unroll
+                for (int r = 0; r < S::ROWS4; ++r) o4[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                const int n4 = n_heads * D / 4;
+#pragma unroll 4
+                for (int i = warp; i < parts; i += kDecWarps) {
+                    const float4 *src = reinterpret_cast<const float4 *>(p.part_o) +
+                                        slot_of(i) * (S::HEADS * D / 4) + lane;
+                    float4 y[S::ROWS4];
+#pragma unroll
+                    for (int r = 0; r < S::ROWS4; ++r)
+                        y[r] = r * 32 + lane < n4 ? __ldcg(src + r * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int r = 0; r < S::ROWS4; ++r) {
+                        const float f = st[i * 3 * S::HEADS + (r * 32 + lane) / (D / 4)];
+                        o4[r].x = fmaf(y[r].x, f, o4[r].x), o4[r].y = fmaf(y[r].y, f, o4[r].y);
+                        o4[r].z = fmaf(y[r].z, f, o4[r].z), o4[r].w = fmaf(y[r].w, f, o4[r].w);
+                    }
+                }
+#pragma unroll
+                for (int r = 0; r < S::ROWS4; ++r)
+                    reinterpret_cast<float4 *>(sum)[(warp * S::ROWS4 + r) * 32 + lane] = o4[r];
+                __syncthreads();
+                for (int x = tid; x < n4; x += kDecThreads) {
                     const int h = x / (D / 4), d = x % (D / 4) * 4;
                     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int i = 0; i < parts; ++i) {
-                        const float f = wt[h * kDecMaxCtas + i];
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(
-                            p.part_o + (static_cast<int64_t>(slot_of(i)) * S::HEADS + h) * D + d));
-                        o.x = fmaf(y.x, f, o.x), o.y = fmaf(y.y, f, o.y);
-                        o.z = fmaf(y.z, f, o.z), o.w = fmaf(y.w, f, o.w);
+#pragma unroll
+                    for (int w = 0; w < kDecWarps; ++w) {
+                        const float4 y = reinterpret_cast<const float4 *>(sum)[w * S::ROWS4 * 32 + x];
+                        o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
                     }
                     const float m = res[h], lm = res[S::HEADS + h], l = res[2 * S::HEADS + h];
                     const float f = l == 0.f ? 0.f : exp2f(m - lm) / l;
