@@ -431,9 +431,9 @@ typedef struct {
 } spava_cache_batch;
 
 /* Workspace bytes of the spava_cache_* calls for this config, whatever the
- * batch.  256-byte aligned, ZERO at first, used by spava_cache_* calls (and
- * spava_device_status) alone: it holds counters that every call returns to
- * zero.  Calls that share it must be ordered (on one stream, or by events). */
+ * batch.  256-byte aligned; its first 256 bytes are the status block, whose
+ * word must start at zero, the rest may hold anything.  Calls that share a
+ * workspace must be ordered (on one stream, or by events). */
 spava_status spava_cache_workspace_size(const spava_cache_config *cfg, size_t *bytes);
 
 /* Writes new_rows rows of every sequence, its last ones: row i of sequence b

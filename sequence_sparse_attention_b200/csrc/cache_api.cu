@@ -62,14 +62,14 @@ spava_status check_rows(const void *p, int64_t stride, int heads, int d) {
     return stride % 8 ? SPAVA_ERR_MISALIGNED : SPAVA_OK;
 }
 
-constexpr size_t kCounterBytes = (sizeof(int32_t) * kDecMaxCtas + 255) / 256 * 256;
+constexpr size_t kCutBytes = sizeof(int4) * kDecMaxCtas;
 
 int head_tile(const spava_cache_config *c) { return c->n_q_heads / c->n_kv_heads > 8 ? 2 : 1; }
 
-// [status block 256 | counters | partial statistics | partial O]
+// [status block 256 | cut items | partial statistics | partial O]
 size_t cache_ws_bytes(const spava_cache_config *c) {
     const size_t heads = 8 * head_tile(c);
-    return 256 + kCounterBytes + sizeof(float) * 2 * kDecMaxCtas * heads * (3 + c->head_dim);
+    return 256 + kCutBytes + sizeof(float) * 2 * kDecMaxCtas * heads * (3 + c->head_dim);
 }
 
 spava_status make_view(const spava_cache_config *c, const spava_cache_pools *p,
@@ -169,16 +169,27 @@ spava_status set_dynamic_smem(K kernel, int bytes, std::atomic<uint64_t> &done, 
 }
 
 template <int D, bool E4M3, int NT>
-spava_status launch_decode(DecodeParams &p, cudaStream_t st) {
+spava_status launch_decode(DecodeParams &p, int64_t max_units, cudaStream_t st) {
     static std::atomic<uint64_t> done{0};
     int dev = 0, n_sm = 0;
     SPAVA_CUDA(cudaGetDevice(&dev));
     SPAVA_CUDA(cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev));
     constexpr int smem = DecodeShape<D, E4M3, NT>::SMEM;
     SPAVA_TRY(set_dynamic_smem(decode_kernel<D, E4M3, NT>, smem, done, dev));
-    const int grid = std::min(2 * n_sm, kDecMaxCtas);
+    // no more blocks than the units of full tables
+    const int grid = static_cast<int>(std::min<int64_t>(std::min(2 * n_sm, kDecMaxCtas), max_units));
     decode_kernel<D, E4M3, NT><<<grid, kDecThreads, smem, st>>>(p);
-    return launched();
+    SPAVA_TRY(launched());
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid * 8 * NT);
+    cfg.blockDim = dim3(kDecThreads);
+    cfg.stream = st;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cuda_ok(cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, p));
 }
 
 }  // namespace
@@ -327,8 +338,8 @@ spava_status spava_cache_attn(const spava_cache_config *cfg, const spava_cache_p
     const double scale = cfg->scale > 0.f ? double(cfg->scale) : 1.0 / std::sqrt(double(cfg->head_dim));
     p.scale_log2 = static_cast<float>(scale * 1.4426950408889634);
     char *at = static_cast<char *>(ws) + 256;
-    p.counters = reinterpret_cast<int *>(at);
-    p.part_stat = reinterpret_cast<float *>(at + kCounterBytes);
+    p.cuts = reinterpret_cast<int4 *>(at);
+    p.part_stat = reinterpret_cast<float *>(at + kCutBytes);
     p.part_o = p.part_stat + size_t(2) * kDecMaxCtas * 3 * 8 * nt;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool e4m3 = cfg->type == SPAVA_CACHE_E4M3;
@@ -336,12 +347,13 @@ spava_status spava_cache_attn(const spava_cache_config *cfg, const spava_cache_p
     const int64_t block = int64_t(kDecWarps) * kDecTileBytes / (2 * cfg->head_dim * (e4m3 ? 1 : 2));
     const int64_t units = (p.cache.cap + block - 1) / block * cfg->n_kv_heads * p.n_hg;
     if (units >= (1LL << 31) / batch->n_seqs) return SPAVA_ERR_UNSUPPORTED;
+    const int64_t all = units * batch->n_seqs;
     if (cfg->head_dim == 64) {
-        if (e4m3) return nt == 1 ? launch_decode<64, true, 1>(p, st) : launch_decode<64, true, 2>(p, st);
-        return nt == 1 ? launch_decode<64, false, 1>(p, st) : launch_decode<64, false, 2>(p, st);
+        if (e4m3) return nt == 1 ? launch_decode<64, true, 1>(p, all, st) : launch_decode<64, true, 2>(p, all, st);
+        return nt == 1 ? launch_decode<64, false, 1>(p, all, st) : launch_decode<64, false, 2>(p, all, st);
     }
-    if (e4m3) return nt == 1 ? launch_decode<128, true, 1>(p, st) : launch_decode<128, true, 2>(p, st);
-    return nt == 1 ? launch_decode<128, false, 1>(p, st) : launch_decode<128, false, 2>(p, st);
+    if (e4m3) return nt == 1 ? launch_decode<128, true, 1>(p, all, st) : launch_decode<128, true, 2>(p, all, st);
+    return nt == 1 ? launch_decode<128, false, 1>(p, all, st) : launch_decode<128, false, 2>(p, all, st);
 }
 
 }  // extern "C"

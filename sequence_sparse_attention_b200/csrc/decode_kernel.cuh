@@ -22,10 +22,20 @@ struct DecodeParams {
     int32_t Hq, G;        // query heads, per KV head
     int32_t n_hg;         // groups of 8 * NT query heads that share a KV head
     float scale_log2;     // softmax scale * log2 e
-    int *counters;        // [kDecMaxCtas], zero between calls
+    int4 *cuts;           // [grid]: the cut item that begins in a block's share: parts (0: none),
+                          // sequence, first query head, query heads
     float *part_stat;     // [2 * kDecMaxCtas][3][8 * NT]
     float *part_o;        // [2 * kDecMaxCtas][8 * NT][D]
 };
+
+// Programmatic dependent launch: the join's blocks are on the SMs, waiting,
+// while the parts are computed.
+__device__ __forceinline__ void launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_primary() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
@@ -117,14 +127,10 @@ struct DecodeShape {
         return ROW >= 128 ? (row >> 1 & 3) * 2 : row >> 1 & 3;
     }
     static constexpr int OPAD = D + 4;                     // floats of an O row in shared memory
-    // The ring is free when a segment is joined, and takes the warps' O and
-    // statistics, then the join's weights.
-    static constexpr int MERGE = kDecWarps * HEADS * (OPAD + 3) * 4 + HEADS * 2 * 4;
+    // The ring is free when a segment ends, and takes the warps' O and statistics.
+    static constexpr int MERGE = kDecWarps * HEADS * (OPAD + 3) * 4;
     static constexpr int ROWS4 = HEADS * D / 128;          // float4s of a partial O per lane of a warp
-    // the join: every part's statistics, the results' statistics, the warps' sums
-    static constexpr int JOIN = (HEADS * (kDecMaxCtas * 3 + 3) + kDecWarps * HEADS * D) * 4;
-    static constexpr int A = MERGE > kDecRingBytes ? MERGE : kDecRingBytes;
-    static constexpr int RING = A > JOIN ? A : JOIN;
+    static constexpr int RING = MERGE > kDecRingBytes ? MERGE : kDecRingBytes;
     // behind it: table entries and, of an e4m3 cache, the words with the rows' exponents
     static constexpr int RW = TT == 64 ? 2 : 1;            // tokens of a tile per lane
     static constexpr int PAGES = kDecPageSlots * RW * 128;         // bytes, a warp
@@ -160,55 +166,76 @@ struct DecodeShape {
 //   - The work of the whole batch is a line of units (BLOCK tokens of one
 //     sequence and KV head), cut into equal shares, one per block, by every
 //     block for itself from the lengths: long and short sequences balance, and
-//     a captured launch follows lengths that change.  A block leaves the parts
-//     of a cut sequence in the workspace, and the last of its blocks to arrive
-//     joins them, in the order of the line: the result does not depend on who
-//     is last.
+//     a captured launch follows lengths that change.  A block leaves its parts
+//     of cut items in the workspace for join_kernel.
 template <int D, bool E4M3, int NT>
 __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_constant__ DecodeParams p) {
     using S = DecodeShape<D, E4M3, NT>;
     extern __shared__ __align__(128) unsigned char smem[];
     __shared__ int s_prefix[kDecThreads + 1];
     __shared__ int s_warp[kDecWarps];
-    __shared__ int s_last;
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int g = lane / 4, c = lane % 4;
     const CacheView &cv = p.cache;
     const int per_seq = cv.Hkv * p.n_hg;  // items (KV head, head group) of a sequence
 
-    // ---- the line of units: thread t holds the sequences [t * per, (t+1) * per)
-    const int per = (cv.n_seqs + kDecThreads - 1) / kDecThreads;
-    int scan = 0;
-    for (int b = tid * per; b < min((tid + 1) * per, cv.n_seqs); ++b)
-        scan += (cache_len(cv, b) + S::BLOCK - 1) / S::BLOCK;
+    launch_dependents();
+
+    // ---- the line of units: sequence groups of `per`, s_prefix[i] the unit where group i begins
+    int per, total;
+    bool empty;  // there are sequences without positions
+    if (cv.n_seqs <= 32) {
+        // every warp for itself, from one load: no barrier
+        per = 1;
+        const int len = lane < cv.n_seqs ? cache_len(cv, lane) : 1;
+        empty = __any_sync(0xffffffffu, len == 0);
+        int scan = lane < cv.n_seqs ? (len + S::BLOCK - 1) / S::BLOCK * per_seq : 0;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, scan, o);
-        if (lane >= o) scan += x;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += x;
+        }
+        s_prefix[lane + 1] = scan;  // the same values from every warp
+        if (lane == 0) s_prefix[0] = 0;
+        __syncwarp();
+        total = __shfl_sync(0xffffffffu, scan, 31);
+    } else {
+        per = (cv.n_seqs + kDecThreads - 1) / kDecThreads;
+        int scan = 0;
+        for (int b = tid * per; b < min((tid + 1) * per, cv.n_seqs); ++b)
+            scan += (cache_len(cv, b) + S::BLOCK - 1) / S::BLOCK;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, scan, o);
+            if (lane >= o) scan += x;
+        }
+        if (lane == 31) s_warp[warp] = scan;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w)
+            if (w < warp) scan += s_warp[w];
+        s_prefix[tid + 1] = scan * per_seq;
+        if (tid == 0) s_prefix[0] = 0;
+        __syncthreads();
+        total = s_prefix[kDecThreads];
+        empty = true;
     }
-    if (lane == 31) s_warp[warp] = scan;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kDecWarps; ++w)
-        if (w < warp) scan += s_warp[w];
-    s_prefix[tid + 1] = scan * per_seq;
-    if (tid == 0) s_prefix[0] = 0;
-    __syncthreads();
-    const int total = s_prefix[kDecThreads];
 
     // ---- sequences without positions
-    for (int b = blockIdx.x; b < cv.n_seqs; b += gridDim.x) {
-        if (cache_len(cv, b) > 0) continue;
-        for (int i = tid; i < p.Hq * D / 8; i += kDecThreads)
-            reinterpret_cast<uint4 *>(p.o + static_cast<int64_t>(b) * p.Hq * D)[i] = make_uint4(0, 0, 0, 0);
-        if (p.lse)
-            for (int h = tid; h < p.Hq; h += kDecThreads)
-                p.lse[static_cast<int64_t>(h) * cv.n_seqs + b] = -INFINITY;
-    }
+    if (empty)
+        for (int b = blockIdx.x; b < cv.n_seqs; b += gridDim.x) {
+            if (cache_len(cv, b) > 0) continue;
+            for (int i = tid; i < p.Hq * D / 8; i += kDecThreads)
+                reinterpret_cast<uint4 *>(p.o + static_cast<int64_t>(b) * p.Hq * D)[i] = make_uint4(0, 0, 0, 0);
+            if (p.lse)
+                for (int h = tid; h < p.Hq; h += kDecThreads)
+                    p.lse[static_cast<int64_t>(h) * cv.n_seqs + b] = -INFINITY;
+        }
 
     // Shares of `base` units, of one more for the first `more` blocks.
     const int ctas = min(total, static_cast<int>(gridDim.x));  // blocks with a share
     const int cta = blockIdx.x;
+    if (tid == 0) p.cuts[cta] = make_int4(0, 0, 0, 0);
     if (cta >= ctas) return;
     const int base = total / ctas, more = total - base * ctas;
     int u = cta * base + min(cta, more);
@@ -221,7 +248,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
     // ---- the sequence of the first unit
     int b, first;  // first: the unit where sequence b begins
     {
-        int lo = 0, hi = kDecThreads;  // s_prefix[lo] <= u < s_prefix[hi]
+        int lo = 0, hi = cv.n_seqs <= 32 ? 32 : kDecThreads;  // s_prefix[lo] <= u < s_prefix[hi]
         while (hi - lo > 1) {
             const int mid = (lo + hi) / 2;
             if (s_prefix[mid] <= u) lo = mid; else hi = mid;
@@ -659,94 +686,97 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
             }
         }
 
-        // ---- join the blocks of a cut item: the last to arrive does it
-        if (!whole) {
-            const int c0 = cta_of(item_u0), parts = cta_of(item_u1 - 1) - c0 + 1;
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                s_last = atomicAdd(p.counters + c0, 1) == parts - 1;
-                __threadfence();
-            }
-            __syncthreads();
-            if (s_last) {
-                float *st = reinterpret_cast<float *>(smem);          // [parts][3][HEADS]: m (then O's weight), lm, l
-                float *res = st + 3 * S::HEADS * kDecMaxCtas;         // [3][HEADS]
-                float *sum = res + 3 * S::HEADS;                      // [warps][HEADS][D]
-                // part 0 is the second one of block c0, the others the first of theirs
-                auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
-                for (int x = tid; x < parts * 3 * S::HEADS; x += kDecThreads) {
-                    const int i = x / (3 * S::HEADS);
-                    st[x] = __ldcg(p.part_stat + slot_of(i) * 3 * S::HEADS + (x - i * 3 * S::HEADS));
-                }
-                __syncthreads();
-                for (int h = warp; h < S::HEADS; h += kDecWarps) {
-                    float m = kDecNone, lm = kDecNone, l = 0.f;
-                    for (int i = lane; i < parts; i += 32) {
-                        m = fmaxf(m, st[i * 3 * S::HEADS + h]);
-                        lm = fmaxf(lm, st[(i * 3 + 1) * S::HEADS + h]);
-                    }
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) {
-                        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        lm = fmaxf(lm, __shfl_xor_sync(0xffffffffu, lm, o));
-                    }
-                    for (int i = lane; i < parts; i += 32) {
-                        st[i * 3 * S::HEADS + h] = exp2_approx(st[i * 3 * S::HEADS + h] - m);
-                        l = fmaf(st[(i * 3 + 2) * S::HEADS + h],
-                                 exp2_approx(st[(i * 3 + 1) * S::HEADS + h] - lm), l);
-                    }
-#pragma unroll
-                    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-                    if (lane == 0) res[h] = m, res[S::HEADS + h] = lm, res[2 * S::HEADS + h] = l;
-                }
-                __syncthreads();
-                // Warp w sums every fourth part, all rows of a part in flight at
-                // once; then the warps' sums, in order.
-                float4 o4[S::ROWS4];
-#pragma unroll
-                for (int r = 0; r < S::ROWS4; ++r) o4[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-                const int n4 = n_heads * D / 4;
-#pragma unroll 4
-                for (int i = warp; i < parts; i += kDecWarps) {
-                    const float4 *src = reinterpret_cast<const float4 *>(p.part_o) +
-                                        slot_of(i) * (S::HEADS * D / 4) + lane;
-                    float4 y[S::ROWS4];
-#pragma unroll
-                    for (int r = 0; r < S::ROWS4; ++r)
-                        y[r] = r * 32 + lane < n4 ? __ldcg(src + r * 32) : make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int r = 0; r < S::ROWS4; ++r) {
-                        const float f = st[i * 3 * S::HEADS + (r * 32 + lane) / (D / 4)];
-                        o4[r].x = fmaf(y[r].x, f, o4[r].x), o4[r].y = fmaf(y[r].y, f, o4[r].y);
-                        o4[r].z = fmaf(y[r].z, f, o4[r].z), o4[r].w = fmaf(y[r].w, f, o4[r].w);
-                    }
-                }
-#pragma unroll
-                for (int r = 0; r < S::ROWS4; ++r)
-                    reinterpret_cast<float4 *>(sum)[(warp * S::ROWS4 + r) * 32 + lane] = o4[r];
-                __syncthreads();
-                for (int x = tid; x < n4; x += kDecThreads) {
-                    const int h = x / (D / 4), d = x % (D / 4) * 4;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-                    for (int w = 0; w < kDecWarps; ++w) {
-                        const float4 y = reinterpret_cast<const float4 *>(sum)[w * S::ROWS4 * 32 + x];
-                        o.x += y.x, o.y += y.y, o.z += y.z, o.w += y.w;
-                    }
-                    const float m = res[h], lm = res[S::HEADS + h], l = res[2 * S::HEADS + h];
-                    const float f = l == 0.f ? 0.f : exp2f(m - lm) / l;
-                    *reinterpret_cast<uint2 *>(p.o + (static_cast<int64_t>(b) * p.Hq + head0 + h) * D + d) =
-                        make_uint2(bf_pack(o.x * f, o.y * f), bf_pack(o.z * f, o.w * f));
-                    if (d == 0 && p.lse)
-                        p.lse[static_cast<int64_t>(head0 + h) * cv.n_seqs + b] =
-                            l == 0.f ? -INFINITY : 0.6931471805599453f * (lm + log2f(l));
-                }
-                if (tid == 0) p.counters[c0] = 0;
-            }
-        }
+        // the join of a cut item goes by the block where it begins
+        if (!whole && u == item_u0 && tid == 0)
+            p.cuts[cta] = make_int4(cta_of(item_u1 - 1) - cta + 1, b, head0, n_heads);
         __syncthreads();  // the ring is free again
         u = seg_end;
+    }
+}
+
+// The parts of the cut items, one block for a block of decode_kernel and a
+// query head: the parts' weights 2^(m_i - max m), the sums, in the order of the
+// line, so that the same call gives the same bytes.  Part 0 is the second one
+// of block c0, the others the first ones of theirs.  Latency bound: a few KB a
+// block, so all of a warp's rows are asked for at once, and each thread works
+// out the statistics that it needs from shared memory.
+template <int D, int NT>
+__global__ void __launch_bounds__(kDecThreads) join_kernel(const __grid_constant__ DecodeParams p) {
+    constexpr int HEADS = 8 * NT, LANES = D / 4, PER = 32 / LANES * kDecWarps;  // parts at a time
+    __shared__ float s_m[kDecMaxCtas], s_lm[kDecMaxCtas], s_l[kDecMaxCtas];
+    __shared__ float4 s_o[kDecThreads];
+    const int tid = threadIdx.x, c0 = blockIdx.x / HEADS, h = blockIdx.x % HEADS;
+    wait_for_primary();
+    const int4 cut = __ldcg(p.cuts + c0);
+    const int parts = cut.x;
+    if (h >= cut.w || parts == 0) return;
+    auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
+    const int l4 = tid % LANES, first = tid / LANES;
+    constexpr int AHEAD = 8;
+    float4 y[AHEAD];  // of the parts first, first + PER, ...
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+        const int i = first + k * PER;
+        y[k] = i < parts ? __ldcg(reinterpret_cast<const float4 *>(p.part_o + (slot_of(i) * HEADS + h) * D) + l4)
+                         : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    for (int i = tid; i < parts; i += kDecThreads) {
+        const float *st = p.part_stat + slot_of(i) * 3 * HEADS + h;
+        s_m[i] = __ldcg(st);
+        s_lm[i] = __ldcg(st + HEADS);
+        s_l[i] = __ldcg(st + 2 * HEADS);
+    }
+    __syncthreads();
+    // every warp the same
+    float m = kDecNone, lm = kDecNone, l = 0.f;
+    const int lane = tid % 32;
+    for (int i = lane; i < parts; i += 32) {
+        m = fmaxf(m, s_m[i]);
+        lm = fmaxf(lm, s_lm[i]);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        lm = fmaxf(lm, __shfl_xor_sync(0xffffffffu, lm, o));
+    }
+    for (int i = lane; i < parts; i += 32) l = fmaf(s_l[i], exp2_approx(s_lm[i] - lm), l);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int at = first; at < parts; at += AHEAD * PER) {
+        if (at != first) {
+#pragma unroll
+            for (int k = 0; k < AHEAD; ++k) {
+                const int i = at + k * PER;
+                y[k] = i < parts
+                           ? __ldcg(reinterpret_cast<const float4 *>(p.part_o + (slot_of(i) * HEADS + h) * D) + l4)
+                           : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < AHEAD; ++k) {
+            const int i = at + k * PER;
+            const float f = i < parts ? exp2_approx(s_m[i] - m) : 0.f;
+            o.x = fmaf(y[k].x, f, o.x), o.y = fmaf(y[k].y, f, o.y);
+            o.z = fmaf(y[k].z, f, o.z), o.w = fmaf(y[k].w, f, o.w);
+        }
+    }
+    s_o[tid] = o;
+    __syncthreads();
+    if (tid < LANES) {
+#pragma unroll
+        for (int w = 1; w < PER; ++w) {
+            const float4 x = s_o[w * LANES + tid];
+            o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+        }
+        const float f = l == 0.f ? 0.f : exp2f(m - lm) / l;
+        const int64_t row = static_cast<int64_t>(cut.y) * p.Hq + cut.z + h;
+        *reinterpret_cast<uint2 *>(p.o + row * D + tid * 4) =
+            make_uint2(bf_pack(o.x * f, o.y * f), bf_pack(o.z * f, o.w * f));
+        if (tid == 0 && p.lse)
+            p.lse[static_cast<int64_t>(cut.z + h) * p.cache.n_seqs + cut.y] =
+                l == 0.f ? -INFINITY : 0.6931471805599453f * (lm + log2f(l));
     }
 }
 
