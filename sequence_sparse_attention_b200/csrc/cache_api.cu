@@ -168,27 +168,44 @@ spava_status set_dynamic_smem(K kernel, int bytes, std::atomic<uint64_t> &done, 
     return SPAVA_OK;
 }
 
+// decode_cluster_kernel takes batches whose items (sequence, KV head, query head
+// group) fit the SMs at once, and whose tables hold at most so many bytes of K and
+// V rows for each block of an item's cluster.
+constexpr int64_t kClusterBlockBytes = 256 << 10;
+
 template <int D, bool E4M3, int NT>
 spava_status launch_decode(DecodeParams &p, int64_t max_units, cudaStream_t st) {
-    static std::atomic<uint64_t> done{0};
+    using S = DecodeShape<D, E4M3, NT>;
+    static std::atomic<uint64_t> done{0}, cluster_done{0};
     int dev = 0, n_sm = 0;
     SPAVA_CUDA(cudaGetDevice(&dev));
     SPAVA_CUDA(cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev));
-    constexpr int smem = DecodeShape<D, E4M3, NT>::SMEM;
-    SPAVA_TRY(set_dynamic_smem(decode_kernel<D, E4M3, NT>, smem, done, dev));
-    // no more blocks than the units of full tables
-    const int grid = static_cast<int>(std::min<int64_t>(std::min(2 * n_sm, kDecMaxCtas), max_units));
-    decode_kernel<D, E4M3, NT><<<grid, kDecThreads, smem, st>>>(p);
-    SPAVA_TRY(launched());
     cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid * 8 * NT);
     cfg.blockDim = dim3(kDecThreads);
     cfg.stream = st;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
+    const int64_t items = int64_t(p.cache.n_seqs) * p.cache.Hkv * p.n_hg;
+    p.cluster = kDecCluster;
+    while (p.cluster > 1 && items * p.cluster > 2 * n_sm) p.cluster /= 2;
+    if (items * p.cluster <= 2 * n_sm && int64_t(p.cache.cap) * 2 * S::ROW <= kClusterBlockBytes * p.cluster) {
+        SPAVA_TRY(set_dynamic_smem(decode_cluster_kernel<D, E4M3, NT>, S::SMEM, cluster_done, dev));
+        attr.id = cudaLaunchAttributeClusterDimension;
+        attr.val.clusterDim.x = p.cluster;
+        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+        cfg.gridDim = dim3(static_cast<unsigned>(items * p.cluster));
+        cfg.dynamicSmemBytes = S::SMEM;
+        return cuda_ok(cudaLaunchKernelEx(&cfg, decode_cluster_kernel<D, E4M3, NT>, p));
+    }
+    SPAVA_TRY(set_dynamic_smem(decode_kernel<D, E4M3, NT>, S::SMEM, done, dev));
+    // no more blocks than the units of full tables
+    const int grid = static_cast<int>(std::min<int64_t>(std::min(2 * n_sm, kDecMaxCtas), max_units));
+    decode_kernel<D, E4M3, NT><<<grid, kDecThreads, S::SMEM, st>>>(p);
+    SPAVA_TRY(launched());
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.gridDim = dim3(grid * 8 * NT);
     return cuda_ok(cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, p));
 }
 

@@ -8,6 +8,7 @@ namespace spava {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kDecCluster = 8;    // most blocks of decode_cluster_kernel's clusters
 constexpr int kDecMaxCtas = 320;  // the workspace's partials are sized for these
 constexpr int kDecStages = 3;
 constexpr int kDecTileBytes = 8192;  // K and V bytes of one warp's tile
@@ -20,6 +21,7 @@ struct DecodeParams {
     __nv_bfloat16 *o;
     float *lse;
     int32_t Hq, G;        // query heads, per KV head
+    int32_t cluster;      // blocks of an item (decode_cluster_kernel): 1, 2, 4 or 8
     int32_t n_hg;         // groups of 8 * NT query heads that share a KV head
     float scale_log2;     // softmax scale * log2 e
     int4 *cuts;           // [grid]: the cut item that begins in a block's share: parts (0: none),
@@ -101,10 +103,51 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t cluster_address(const void *mine, uint32_t rank) {
+    uint32_t r;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;"
+        : "=r"(r)
+        : "r"(static_cast<uint32_t>(__cvta_generic_to_shared(mine))), "r"(rank));
+    return r;
+}
+__device__ __forceinline__ float cluster_load(uint32_t a) {
+    float r;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(a) : "memory");
+    return r;
+}
+__device__ __forceinline__ float4 cluster_load4(uint32_t a) {
+    float4 r;
+    asm volatile("ld.shared::cluster.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w)
+                 : "r"(a)
+                 : "memory");
+    return r;
+}
+__device__ __forceinline__ void add_part(float4 &o, const float4 &y, float f) {
+    o.x = fmaf(y.x, f, o.x), o.y = fmaf(y.y, f, o.y);
+    o.z = fmaf(y.z, f, o.z), o.w = fmaf(y.w, f, o.w);
+}
+
 // The state of a softmax over part of a context, in base 2: l = sum 2^(s - lm),
 // O = sum 2^(s + e - m) v with e the value's exponent (m = lm where there is
 // none).  kDecNone marks a part without a finite score.
 constexpr float kDecNone = -3.402823466e38f;
+
+// Four elements of a query head's output, and with the first its lse, from the
+// whole context's state.
+template <int D>
+__device__ __forceinline__ void store_result(const DecodeParams &p, int b, int head, int d, float m, float lm,
+                                             float l, const float4 &o) {
+    const float f = l == 0.f ? 0.f : exp2f(m - lm) / l;
+    *reinterpret_cast<uint2 *>(p.o + (static_cast<int64_t>(b) * p.Hq + head) * D + d) =
+        make_uint2(bf_pack(o.x * f, o.y * f), bf_pack(o.z * f, o.w * f));
+    if (d == 0 && p.lse)
+        p.lse[static_cast<int64_t>(head) * p.cache.n_seqs + b] =
+            l == 0.f ? -INFINITY : 0.6931471805599453f * (lm + log2f(l));
+}
 
 template <int D, bool E4M3, int NT>
 struct DecodeShape {
@@ -168,115 +211,26 @@ struct DecodeShape {
 //     block for itself from the lengths: long and short sequences balance, and
 //     a captured launch follows lengths that change.  A block leaves its parts
 //     of cut items in the workspace for join_kernel.
-template <int D, bool E4M3, int NT>
-__global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_constant__ DecodeParams p) {
+template <int D, bool E4M3, int NT, bool CLUSTER>
+__device__ __forceinline__ void decode_body(const DecodeParams &p) {
     using S = DecodeShape<D, E4M3, NT>;
     extern __shared__ __align__(128) unsigned char smem[];
-    __shared__ int s_prefix[kDecThreads + 1];
-    __shared__ int s_warp[kDecWarps];
     const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
     const int g = lane / 4, c = lane % 4;
     const CacheView &cv = p.cache;
     const int per_seq = cv.Hkv * p.n_hg;  // items (KV head, head group) of a sequence
 
-    launch_dependents();
-
-    // ---- the line of units: sequence groups of `per`, s_prefix[i] the unit where group i begins
-    int per, total;
-    bool empty;  // there are sequences without positions
-    if (cv.n_seqs <= 32) {
-        // every warp for itself, from one load: no barrier
-        per = 1;
-        const int len = lane < cv.n_seqs ? cache_len(cv, lane) : 1;
-        empty = __any_sync(0xffffffffu, len == 0);
-        int scan = lane < cv.n_seqs ? (len + S::BLOCK - 1) / S::BLOCK * per_seq : 0;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, scan, o);
-            if (lane >= o) scan += x;
-        }
-        s_prefix[lane + 1] = scan;  // the same values from every warp
-        if (lane == 0) s_prefix[0] = 0;
-        __syncwarp();
-        total = __shfl_sync(0xffffffffu, scan, 31);
-    } else {
-        per = (cv.n_seqs + kDecThreads - 1) / kDecThreads;
-        int scan = 0;
-        for (int b = tid * per; b < min((tid + 1) * per, cv.n_seqs); ++b)
-            scan += (cache_len(cv, b) + S::BLOCK - 1) / S::BLOCK;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int x = __shfl_up_sync(0xffffffffu, scan, o);
-            if (lane >= o) scan += x;
-        }
-        if (lane == 31) s_warp[warp] = scan;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kDecWarps; ++w)
-            if (w < warp) scan += s_warp[w];
-        s_prefix[tid + 1] = scan * per_seq;
-        if (tid == 0) s_prefix[0] = 0;
-        __syncthreads();
-        total = s_prefix[kDecThreads];
-        empty = true;
-    }
-
-    // ---- sequences without positions
-    if (empty)
-        for (int b = blockIdx.x; b < cv.n_seqs; b += gridDim.x) {
-            if (cache_len(cv, b) > 0) continue;
-            for (int i = tid; i < p.Hq * D / 8; i += kDecThreads)
-                reinterpret_cast<uint4 *>(p.o + static_cast<int64_t>(b) * p.Hq * D)[i] = make_uint4(0, 0, 0, 0);
-            if (p.lse)
-                for (int h = tid; h < p.Hq; h += kDecThreads)
-                    p.lse[static_cast<int64_t>(h) * cv.n_seqs + b] = -INFINITY;
-        }
-
-    // Shares of `base` units, of one more for the first `more` blocks.
-    const int ctas = min(total, static_cast<int>(gridDim.x));  // blocks with a share
-    const int cta = blockIdx.x;
-    if (tid == 0) p.cuts[cta] = make_int4(0, 0, 0, 0);
-    if (cta >= ctas) return;
-    const int base = total / ctas, more = total - base * ctas;
-    int u = cta * base + min(cta, more);
-    const int u_end = u + base + (cta < more ? 1 : 0);
-    auto cta_of = [&](int x) {
-        const int y = x - more * (base + 1);
-        return y < 0 ? x / (base + 1) : more + y / base;
-    };
-
-    // ---- the sequence of the first unit
-    int b, first;  // first: the unit where sequence b begins
-    {
-        int lo = 0, hi = cv.n_seqs <= 32 ? 32 : kDecThreads;  // s_prefix[lo] <= u < s_prefix[hi]
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) / 2;
-            if (s_prefix[mid] <= u) lo = mid; else hi = mid;
-        }
-        b = lo * per;
-        first = s_prefix[lo];
-    }
-    int len = cache_len(cv, b);
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) +
                           warp * (kDecStages * kDecTileBytes);
     const uint32_t side = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + S::RING +
                           warp * (S::PAGES + S::EXPS) + lane * 4;
 
-    while (u < u_end) {
-        int blocks = (len + S::BLOCK - 1) / S::BLOCK;
-        while (u >= first + blocks * per_seq) {
-            first += blocks * per_seq;
-            len = cache_len(cv, ++b);
-            blocks = (len + S::BLOCK - 1) / S::BLOCK;
-        }
-        const int item = (u - first) / blocks;
-        const int item_u0 = first + item * blocks, item_u1 = item_u0 + blocks;
-        const int kvh = item / p.n_hg, hg = item - kvh * p.n_hg;
-        const int seg_end = min(u_end, item_u1);
-        const int n = seg_end - u;                           // tiles of this warp
-        const int t0 = (u - item_u0) * S::BLOCK + warp * S::TT;  // first token of tile 0
-        const int head0 = kvh * p.G + hg * S::HEADS;
-        const int n_heads = min(S::HEADS, p.G - hg * S::HEADS);
+    // ---- the softmax over some of an item's tokens: the tiles t0 + i * STEP, i < n,
+    // of every warp; leaves the warps' states in shared memory
+    const int STEP = CLUSTER ? p.cluster * S::BLOCK : S::BLOCK;
+    float *sm_o = reinterpret_cast<float *>(smem);          // [warps][HEADS][OPAD]
+    float *sm_st = sm_o + kDecWarps * S::HEADS * S::OPAD;   // [3][warps][HEADS]: m, lm, l
+    auto segment = [&](int b, int len, int kvh, int head0, int n_heads, int t0, int n) {
         const uint32_t head_rows = static_cast<uint32_t>(kvh) * cv.page.d;
 
         // ---- q: the MMA's B operand, and its scale
@@ -346,7 +300,7 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
         constexpr int RW = S::RW, K = kDecStages - 1;
         const int32_t *table = cv.table + b * cv.max_pages;
         auto token = [&](int i, int k) {
-            return static_cast<int64_t>(t0) + static_cast<int64_t>(i) * S::BLOCK +
+            return static_cast<int64_t>(t0) + static_cast<int64_t>(i) * STEP +
                    (S::TT == 16 ? lane % 16 : lane + 32 * k);
         };
         auto held_token = [&](int i, int64_t t) { return i < n && t < len; };
@@ -624,8 +578,6 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
         cp_async_wait<0>();
 
         // ---- join the warps of the block
-        float *sm_o = reinterpret_cast<float *>(smem);                    // [warps][HEADS][OPAD]
-        float *sm_st = sm_o + kDecWarps * S::HEADS * S::OPAD;             // [3][warps][HEADS]: m, lm, l
         __syncthreads();
 #pragma unroll
         for (int t = 0; t < NT; ++t)
@@ -648,50 +600,212 @@ __global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_consta
                 }
             }
         __syncthreads();
-        const bool whole = u == item_u0 && seg_end == item_u1;
-        const int part = 2 * cta + (u == item_u0 ? 1 : 0);
-        // thread: one head of 4 floats of d at a time
+    };
+    // the block's state of one head and 4 floats of d
+    auto block_state = [&](int h, int d, float &m, float &lm, float &l, float4 &o) {
+        m = lm = kDecNone;
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+            m = fmaxf(m, sm_st[w * S::HEADS + h]);
+            lm = fmaxf(lm, sm_st[(kDecWarps + w) * S::HEADS + h]);
+        }
+        l = 0.f;
+        o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kDecWarps; ++w) {
+            l = fmaf(sm_st[(2 * kDecWarps + w) * S::HEADS + h],
+                     exp2_approx(sm_st[(kDecWarps + w) * S::HEADS + h] - lm), l);
+            add_part(o, *reinterpret_cast<const float4 *>(sm_o + (w * S::HEADS + h) * S::OPAD + d),
+                     exp2_approx(sm_st[w * S::HEADS + h] - m));
+        }
+    };
+    if constexpr (!CLUSTER) {
+        __shared__ int s_prefix[kDecThreads + 1];
+        __shared__ int s_warp[kDecWarps];
+        launch_dependents();
+    
+        // ---- the line of units: sequence groups of `per`, s_prefix[i] the unit where group i begins
+        int per, total;
+        bool empty;  // there are sequences without positions
+        if (cv.n_seqs <= 32) {
+            // every warp for itself, from one load: no barrier
+            per = 1;
+            const int len = lane < cv.n_seqs ? cache_len(cv, lane) : 1;
+            empty = __any_sync(0xffffffffu, len == 0);
+            int scan = lane < cv.n_seqs ? (len + S::BLOCK - 1) / S::BLOCK * per_seq : 0;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, scan, o);
+                if (lane >= o) scan += x;
+            }
+            s_prefix[lane + 1] = scan;  // the same values from every warp
+            if (lane == 0) s_prefix[0] = 0;
+            __syncwarp();
+            total = __shfl_sync(0xffffffffu, scan, 31);
+        } else {
+            per = (cv.n_seqs + kDecThreads - 1) / kDecThreads;
+            int scan = 0;
+            for (int b = tid * per; b < min((tid + 1) * per, cv.n_seqs); ++b)
+                scan += (cache_len(cv, b) + S::BLOCK - 1) / S::BLOCK;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int x = __shfl_up_sync(0xffffffffu, scan, o);
+                if (lane >= o) scan += x;
+            }
+            if (lane == 31) s_warp[warp] = scan;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < kDecWarps; ++w)
+                if (w < warp) scan += s_warp[w];
+            s_prefix[tid + 1] = scan * per_seq;
+            if (tid == 0) s_prefix[0] = 0;
+            __syncthreads();
+            total = s_prefix[kDecThreads];
+            empty = true;
+        }
+    
+        // ---- sequences without positions
+        if (empty)
+            for (int b = blockIdx.x; b < cv.n_seqs; b += gridDim.x) {
+                if (cache_len(cv, b) > 0) continue;
+                for (int i = tid; i < p.Hq * D / 8; i += kDecThreads)
+                    reinterpret_cast<uint4 *>(p.o + static_cast<int64_t>(b) * p.Hq * D)[i] = make_uint4(0, 0, 0, 0);
+                if (p.lse)
+                    for (int h = tid; h < p.Hq; h += kDecThreads)
+                        p.lse[static_cast<int64_t>(h) * cv.n_seqs + b] = -INFINITY;
+            }
+    
+        // Shares of `base` units, of one more for the first `more` blocks.
+        const int ctas = min(total, static_cast<int>(gridDim.x));  // blocks with a share
+        const int cta = blockIdx.x;
+        if (tid == 0) p.cuts[cta] = make_int4(0, 0, 0, 0);
+        if (cta >= ctas) return;
+        const int base = total / ctas, more = total - base * ctas;
+        int u = cta * base + min(cta, more);
+        const int u_end = u + base + (cta < more ? 1 : 0);
+        auto cta_of = [&](int x) {
+            const int y = x - more * (base + 1);
+            return y < 0 ? x / (base + 1) : more + y / base;
+        };
+    
+        // ---- the sequence of the first unit
+        int b, first;  // first: the unit where sequence b begins
+        {
+            int lo = 0, hi = cv.n_seqs <= 32 ? 32 : kDecThreads;  // s_prefix[lo] <= u < s_prefix[hi]
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) / 2;
+                if (s_prefix[mid] <= u) lo = mid; else hi = mid;
+            }
+            b = lo * per;
+            first = s_prefix[lo];
+        }
+        int len = cache_len(cv, b);
+
+        while (u < u_end) {
+            int blocks = (len + S::BLOCK - 1) / S::BLOCK;
+            while (u >= first + blocks * per_seq) {
+                first += blocks * per_seq;
+                len = cache_len(cv, ++b);
+                blocks = (len + S::BLOCK - 1) / S::BLOCK;
+            }
+            const int item = (u - first) / blocks;
+            const int item_u0 = first + item * blocks, item_u1 = item_u0 + blocks;
+            const int kvh = item / p.n_hg, hg = item - kvh * p.n_hg;
+            const int seg_end = min(u_end, item_u1);
+            const int n = seg_end - u;                           // tiles of this warp
+            const int t0 = (u - item_u0) * S::BLOCK + warp * S::TT;  // first token of tile 0
+            const int head0 = kvh * p.G + hg * S::HEADS;
+            const int n_heads = min(S::HEADS, p.G - hg * S::HEADS);
+            segment(b, len, kvh, head0, n_heads, t0, n);
+            const bool whole = u == item_u0 && seg_end == item_u1;
+            const int part = 2 * cta + (u == item_u0 ? 1 : 0);
+            for (int x = tid; x < S::HEADS * D / 4; x += kDecThreads) {
+                const int h = x / (D / 4), d = x % (D / 4) * 4;
+                float m, lm, l;
+                float4 o;
+                block_state(h, d, m, lm, l, o);
+                if (!whole) {
+                    if (d == 0) {
+                        float *st = p.part_stat + part * 3 * S::HEADS + h;
+                        st[0] = m, st[S::HEADS] = lm, st[2 * S::HEADS] = l;
+                    }
+                    reinterpret_cast<float4 *>(p.part_o + (part * S::HEADS + h) * D + d)[0] = o;
+                } else if (h < n_heads) {
+                    store_result<D>(p, b, head0 + h, d, m, lm, l, o);
+                }
+            }
+            // the join of a cut item goes by the block where it begins
+            if (!whole && u == item_u0 && tid == 0)
+                p.cuts[cta] = make_int4(cta_of(item_u1 - 1) - cta + 1, b, head0, n_heads);
+            __syncthreads();  // the ring is free again
+            u = seg_end;
+        }
+    } else {
+        const uint32_t item = blockIdx.x / p.cluster, rank = blockIdx.x - item * p.cluster;
+        const int b = item / per_seq, in_seq = item - b * per_seq;
+        const int kvh = in_seq / p.n_hg, hg = in_seq - kvh * p.n_hg;
+        const int head0 = kvh * p.G + hg * S::HEADS;
+        const int n_heads = min(S::HEADS, p.G - hg * S::HEADS);
+        const int len = cache_len(cv, b);
+        const int blocks = (len + S::BLOCK - 1) / S::BLOCK;
+        segment(b, len, kvh, head0, n_heads, rank * S::BLOCK + warp * S::TT,
+                (blocks + p.cluster - 1 - static_cast<int>(rank)) / p.cluster);
+        // the block's state, for the others to read
+        float *cl_o = sm_st + 3 * kDecWarps * S::HEADS;  // [HEADS][D]
+        float *cl_st = cl_o + S::HEADS * D;              // [3][HEADS]
         for (int x = tid; x < S::HEADS * D / 4; x += kDecThreads) {
             const int h = x / (D / 4), d = x % (D / 4) * 4;
-            float m = kDecNone, lm = kDecNone;
+            float m, lm, l;
+            float4 o;
+            block_state(h, d, m, lm, l, o);
+            reinterpret_cast<float4 *>(cl_o)[x] = o;
+            if (d == 0) cl_st[h] = m, cl_st[S::HEADS + h] = lm, cl_st[2 * S::HEADS + h] = l;
+        }
+        cluster_sync();
+        const int share = S::HEADS * D / 4 / p.cluster;  // float4s of the result that a block writes
+        for (int i = tid; i < share; i += kDecThreads) {
+            const int x = rank * share + i, h = x / (D / 4), d = x % (D / 4) * 4;
+            if (h >= n_heads) break;
+            float ms[kDecCluster], lms[kDecCluster], ls[kDecCluster];
+            float4 os[kDecCluster];
 #pragma unroll
-            for (int w = 0; w < kDecWarps; ++w) {
-                m = fmaxf(m, sm_st[w * S::HEADS + h]);
-                lm = fmaxf(lm, sm_st[(kDecWarps + w) * S::HEADS + h]);
+            for (int r = 0; r < kDecCluster; ++r) {
+                ms[r] = lms[r] = kDecNone, ls[r] = 0.f, os[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (r < p.cluster) {
+                    const uint32_t st = cluster_address(cl_st + h, r);
+                    ms[r] = cluster_load(st);
+                    lms[r] = cluster_load(st + 4 * S::HEADS);
+                    ls[r] = cluster_load(st + 8 * S::HEADS);
+                    os[r] = cluster_load4(cluster_address(cl_o + 4 * x, r));
+                }
             }
-            float l = 0.f;
+            float m = kDecNone, lm = kDecNone, l = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-            for (int w = 0; w < kDecWarps; ++w) {
-                const float f = exp2_approx(sm_st[w * S::HEADS + h] - m);
-                l = fmaf(sm_st[(2 * kDecWarps + w) * S::HEADS + h],
-                         exp2_approx(sm_st[(kDecWarps + w) * S::HEADS + h] - lm), l);
-                const float4 y = *reinterpret_cast<const float4 *>(sm_o + (w * S::HEADS + h) * S::OPAD + d);
-                o.x = fmaf(y.x, f, o.x), o.y = fmaf(y.y, f, o.y);
-                o.z = fmaf(y.z, f, o.z), o.w = fmaf(y.w, f, o.w);
+            for (int r = 0; r < kDecCluster; ++r) m = fmaxf(m, ms[r]), lm = fmaxf(lm, lms[r]);
+#pragma unroll
+            for (int r = 0; r < kDecCluster; ++r) {
+                l = fmaf(ls[r], exp2_approx(lms[r] - lm), l);
+                add_part(o, os[r], exp2_approx(ms[r] - m));
             }
-            if (!whole) {
-                if (d == 0) {
-                    float *st = p.part_stat + static_cast<int64_t>(part) * 3 * S::HEADS + h;
-                    st[0] = m, st[S::HEADS] = lm, st[2 * S::HEADS] = l;
-                }
-                reinterpret_cast<float4 *>(p.part_o + (static_cast<int64_t>(part) * S::HEADS + h) * D + d)[0] = o;
-            } else if (h < n_heads) {
-                const float f = l == 0.f ? 0.f : exp2f(m - lm) / l;
-                *reinterpret_cast<uint2 *>(p.o + (static_cast<int64_t>(b) * p.Hq + head0 + h) * D + d) =
-                    make_uint2(bf_pack(o.x * f, o.y * f), bf_pack(o.z * f, o.w * f));
-                if (d == 0 && p.lse)
-                    p.lse[static_cast<int64_t>(head0 + h) * cv.n_seqs + b] =
-                        l == 0.f ? -INFINITY : 0.6931471805599453f * (lm + log2f(l));
-            }
+            store_result<D>(p, b, head0 + h, d, m, lm, l, o);
         }
-
-        // the join of a cut item goes by the block where it begins
-        if (!whole && u == item_u0 && tid == 0)
-            p.cuts[cta] = make_int4(cta_of(item_u1 - 1) - cta + 1, b, head0, n_heads);
-        __syncthreads();  // the ring is free again
-        u = seg_end;
+        cluster_sync();  // no block leaves while it is read
     }
+}
+
+template <int D, bool E4M3, int NT>
+__global__ void __launch_bounds__(kDecThreads) decode_kernel(const __grid_constant__ DecodeParams p) {
+    decode_body<D, E4M3, NT, false>(p);
+}
+
+// Short contexts: an item is one cluster's, block after block of tokens in turn,
+// and the blocks' states are joined through distributed shared memory.  One
+// launch, no line, no parts in memory.
+template <int D, bool E4M3, int NT>
+__global__ void __launch_bounds__(kDecThreads)
+    decode_cluster_kernel(const __grid_constant__ DecodeParams p) {
+    decode_body<D, E4M3, NT, true>(p);
 }
 
 // The parts of the cut items, one block for a block of decode_kernel and a
@@ -757,9 +871,7 @@ __global__ void __launch_bounds__(kDecThreads) join_kernel(const __grid_constant
 #pragma unroll
         for (int k = 0; k < AHEAD; ++k) {
             const int i = at + k * PER;
-            const float f = i < parts ? exp2_approx(s_m[i] - m) : 0.f;
-            o.x = fmaf(y[k].x, f, o.x), o.y = fmaf(y[k].y, f, o.y);
-            o.z = fmaf(y[k].z, f, o.z), o.w = fmaf(y[k].w, f, o.w);
+            add_part(o, y[k], i < parts ? exp2_approx(s_m[i] - m) : 0.f);
         }
     }
     s_o[tid] = o;
@@ -770,13 +882,7 @@ __global__ void __launch_bounds__(kDecThreads) join_kernel(const __grid_constant
             const float4 x = s_o[w * LANES + tid];
             o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
         }
-        const float f = l == 0.f ? 0.f : exp2f(m - lm) / l;
-        const int64_t row = static_cast<int64_t>(cut.y) * p.Hq + cut.z + h;
-        *reinterpret_cast<uint2 *>(p.o + row * D + tid * 4) =
-            make_uint2(bf_pack(o.x * f, o.y * f), bf_pack(o.z * f, o.w * f));
-        if (tid == 0 && p.lse)
-            p.lse[static_cast<int64_t>(cut.z + h) * p.cache.n_seqs + cut.y] =
-                l == 0.f ? -INFINITY : 0.6931471805599453f * (lm + log2f(l));
+        store_result<D>(p, cut.y, cut.z + h, tid * 4, m, lm, l, o);
     }
 }
 

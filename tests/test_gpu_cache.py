@@ -265,10 +265,21 @@ ATTN_CASES = [
 ]
 
 
+def widen(table, page, tokens=1 << 17):
+    """The same table with room for more tokens (entries that are not read):
+    short contexts then run as long ones may."""
+    wide = torch.full((table.shape[0], -(-tokens // page)), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table[:, :wide.shape[1]]
+    return wide
+
+
+@pytest.mark.parametrize("wide", [False, True])
 @pytest.mark.parametrize("kind", ["bf16", "e4m3"])
 @pytest.mark.parametrize("lens,Hq,Hkv,d,page", ATTN_CASES)
-def test_attn(lens, Hq, Hkv, d, page, kind):
+def test_attn(lens, Hq, Hkv, d, page, kind, wide):
     cache, pools, q, table, lt = attn_case(lens, Hq, Hkv, d, page, kind == "e4m3", seed=len(lens) + Hq)
+    if wide:
+        table = widen(table, page)
     o, lse = cache.attn(q, table, lt)
     assert cache.device_status() == 0
     cu.check_attn(o, lse, q, pools, table, lens, page)
