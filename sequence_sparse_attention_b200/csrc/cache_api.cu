@@ -201,12 +201,16 @@ spava_status launch_decode(DecodeParams &p, int64_t max_units, cudaStream_t st) 
     SPAVA_TRY(set_dynamic_smem(decode_kernel<D, E4M3, NT>, S::SMEM, done, dev));
     // no more blocks than the units of full tables
     const int grid = static_cast<int>(std::min<int64_t>(std::min(2 * n_sm, kDecMaxCtas), max_units));
+    p.cuts_by_item = items <= grid;
     decode_kernel<D, E4M3, NT><<<grid, kDecThreads, S::SMEM, st>>>(p);
     SPAVA_TRY(launched());
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.gridDim = dim3(grid * 8 * NT);
-    return cuda_ok(cudaLaunchKernelEx(&cfg, join_kernel<D, NT>, p));
+    const int cuts = static_cast<int>(std::min<int64_t>(items, grid));
+    const bool split = cuts * 8 * NT <= grid;
+    cfg.gridDim = dim3(split ? cuts * 8 * NT : cuts);
+    return cuda_ok(split ? cudaLaunchKernelEx(&cfg, join_kernel<D, NT, true>, p)
+                         : cudaLaunchKernelEx(&cfg, join_kernel<D, NT, false>, p));
 }
 
 }  // namespace

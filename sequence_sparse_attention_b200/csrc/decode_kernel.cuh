@@ -24,8 +24,11 @@ struct DecodeParams {
     int32_t cluster;      // blocks of an item (decode_cluster_kernel): 1, 2, 4 or 8
     int32_t n_hg;         // groups of 8 * NT query heads that share a KV head
     float scale_log2;     // softmax scale * log2 e
-    int4 *cuts;           // [grid]: the cut item that begins in a block's share: parts (0: none),
-                          // sequence, first query head, query heads
+    // [min(items, grid)]: an item's first block and number of parts, or of the
+    // item that is cut and begins in a block's share where those are fewer; no
+    // parts: not cut.  And its sequence and head group.
+    int4 *cuts;
+    int32_t cuts_by_item;
     float *part_stat;     // [2 * kDecMaxCtas][3][8 * NT]
     float *part_o;        // [2 * kDecMaxCtas][8 * NT][D]
 };
@@ -673,12 +676,14 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
                 if (p.lse)
                     for (int h = tid; h < p.Hq; h += kDecThreads)
                         p.lse[static_cast<int64_t>(h) * cv.n_seqs + b] = -INFINITY;
+                if (p.cuts_by_item)
+                    for (int i = tid; i < per_seq; i += kDecThreads) p.cuts[b * per_seq + i] = make_int4(0, 0, 0, 0);
             }
     
         // Shares of `base` units, of one more for the first `more` blocks.
         const int ctas = min(total, static_cast<int>(gridDim.x));  // blocks with a share
         const int cta = blockIdx.x;
-        if (tid == 0) p.cuts[cta] = make_int4(0, 0, 0, 0);
+        if (tid == 0 && !p.cuts_by_item) p.cuts[cta] = make_int4(0, 0, 0, 0);
         if (cta >= ctas) return;
         const int base = total / ctas, more = total - base * ctas;
         int u = cta * base + min(cta, more);
@@ -734,9 +739,9 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
                     store_result<D>(p, b, head0 + h, d, m, lm, l, o);
                 }
             }
-            // the join of a cut item goes by the block where it begins
-            if (!whole && u == item_u0 && tid == 0)
-                p.cuts[cta] = make_int4(cta_of(item_u1 - 1) - cta + 1, b, head0, n_heads);
+            if (u == item_u0 && tid == 0 && (p.cuts_by_item || !whole))
+                p.cuts[p.cuts_by_item ? b * per_seq + item : cta] =
+                    make_int4(cta, whole ? 0 : cta_of(item_u1 - 1) - cta + 1, b, item);
             __syncthreads();  // the ring is free again
             u = seg_end;
         }
@@ -808,81 +813,80 @@ __global__ void __launch_bounds__(kDecThreads)
     decode_body<D, E4M3, NT, true>(p);
 }
 
-// The parts of the cut items, one block for a block of decode_kernel and a
-// query head: the parts' weights 2^(m_i - max m), the sums, in the order of the
-// line, so that the same call gives the same bytes.  Part 0 is the second one
-// of block c0, the others the first ones of theirs.  Latency bound: a few KB a
-// block, so all of a warp's rows are asked for at once, and each thread works
-// out the statistics that it needs from shared memory.
-template <int D, int NT>
+// The parts of the cut items, weighted by 2^(m_i - max m) and summed in the order
+// of the line, so that the same call gives the same bytes.  Part 0 is the second
+// one of the item's first block, the others the first ones of the blocks behind.
+// It is bound by latency -- a dependent launch, two reads of L2 --, so everything
+// that a thread needs is asked for at once: LANES threads hold a row of O, and
+// work out its statistics among themselves, without shared memory.
+// SPLIT: a block is one query head of an item, its threads split the parts (few
+// items, many parts each: 128K tokens on 4 KV heads are 74 parts an item).
+// Otherwise a block is an item (many items of two or three parts).
+template <int D, int NT, bool SPLIT>
 __global__ void __launch_bounds__(kDecThreads) join_kernel(const __grid_constant__ DecodeParams p) {
-    constexpr int HEADS = 8 * NT, LANES = D / 4, PER = 32 / LANES * kDecWarps;  // parts at a time
-    __shared__ float s_m[kDecMaxCtas], s_lm[kDecMaxCtas], s_l[kDecMaxCtas];
+    constexpr int HEADS = 8 * NT, LANES = D / 4, GROUPS = kDecThreads / LANES;
+    constexpr int PER = SPLIT ? GROUPS : 1;  // threads that share a column's parts
+    constexpr int AHEAD = SPLIT ? 8 : 4;
     __shared__ float4 s_o[kDecThreads];
-    const int tid = threadIdx.x, c0 = blockIdx.x / HEADS, h = blockIdx.x % HEADS;
+    const int tid = threadIdx.x, l4 = tid % LANES, group = tid / LANES;
     wait_for_primary();
-    const int4 cut = __ldcg(p.cuts + c0);
-    const int parts = cut.x;
-    if (h >= cut.w || parts == 0) return;
+    const int4 cut = __ldcg(p.cuts + (SPLIT ? blockIdx.x / HEADS : blockIdx.x));
+    const int c0 = cut.x, parts = cut.y;
+    if (parts == 0) return;
+    const int kvh = cut.w / p.n_hg, hg = cut.w - kvh * p.n_hg;
+    const int head0 = kvh * p.G + hg * HEADS, n_heads = min(HEADS, p.G - hg * HEADS);
+    const int first = SPLIT ? group : 0;
     auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
-    const int l4 = tid % LANES, first = tid / LANES;
-    constexpr int AHEAD = 8;
-    float4 y[AHEAD];  // of the parts first, first + PER, ...
-#pragma unroll
-    for (int k = 0; k < AHEAD; ++k) {
-        const int i = first + k * PER;
-        y[k] = i < parts ? __ldcg(reinterpret_cast<const float4 *>(p.part_o + (slot_of(i) * HEADS + h) * D) + l4)
-                         : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
-    for (int i = tid; i < parts; i += kDecThreads) {
-        const float *st = p.part_stat + slot_of(i) * 3 * HEADS + h;
-        s_m[i] = __ldcg(st);
-        s_lm[i] = __ldcg(st + HEADS);
-        s_l[i] = __ldcg(st + 2 * HEADS);
-    }
-    __syncthreads();
-    // every warp the same
-    float m = kDecNone, lm = kDecNone, l = 0.f;
-    const int lane = tid % 32;
-    for (int i = lane; i < parts; i += 32) {
-        m = fmaxf(m, s_m[i]);
-        lm = fmaxf(lm, s_lm[i]);
-    }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        lm = fmaxf(lm, __shfl_xor_sync(0xffffffffu, lm, o));
-    }
-    for (int i = lane; i < parts; i += 32) l = fmaf(s_l[i], exp2_approx(s_lm[i] - lm), l);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
 
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int at = first; at < parts; at += AHEAD * PER) {
-        if (at != first) {
+    for (int h = SPLIT ? blockIdx.x % HEADS : group; h < n_heads; h += SPLIT ? HEADS : GROUPS) {
+        float4 y[AHEAD];
+        float w[AHEAD];
+        auto load = [&](int at) {
 #pragma unroll
             for (int k = 0; k < AHEAD; ++k) {
                 const int i = at + k * PER;
-                y[k] = i < parts
-                           ? __ldcg(reinterpret_cast<const float4 *>(p.part_o + (slot_of(i) * HEADS + h) * D) + l4)
-                           : make_float4(0.f, 0.f, 0.f, 0.f);
+                y[k] = make_float4(0.f, 0.f, 0.f, 0.f), w[k] = kDecNone;
+                if (i < parts) {
+                    y[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + (slot_of(i) * HEADS + h) * D) + l4);
+                    w[k] = __ldcg(p.part_stat + slot_of(i) * 3 * HEADS + h);
+                }
             }
+        };
+        load(first);
+        // the item's statistics: a lane's parts in turn, then the lanes'
+        float m = kDecNone, lm = kDecNone, l = 0.f;
+#pragma unroll 4
+        for (int i = l4; i < parts; i += LANES) {
+            const float *st = p.part_stat + slot_of(i) * 3 * HEADS + h;
+            const float mi = __ldcg(st), lmi = __ldcg(st + HEADS), li = __ldcg(st + 2 * HEADS);
+            const float top = fmaxf(lm, lmi);
+            l = l * exp2_approx(lm - top) + li * exp2_approx(lmi - top);
+            lm = top;
+            m = fmaxf(m, mi);
         }
+        const unsigned mates = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << (tid % 32 / LANES * LANES);
 #pragma unroll
-        for (int k = 0; k < AHEAD; ++k) {
-            const int i = at + k * PER;
-            add_part(o, y[k], i < parts ? exp2_approx(s_m[i] - m) : 0.f);
+        for (int o = 1; o < LANES; o <<= 1) {
+            const float lmi = __shfl_xor_sync(mates, lm, o), li = __shfl_xor_sync(mates, l, o);
+            const float top = fmaxf(lm, lmi);
+            l = l * exp2_approx(lm - top) + li * exp2_approx(lmi - top);
+            lm = top;
+            m = fmaxf(m, __shfl_xor_sync(mates, m, o));
         }
-    }
-    s_o[tid] = o;
-    __syncthreads();
-    if (tid < LANES) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int at = first; at < parts; at += AHEAD * PER) {
+            if (at != first) load(at);
 #pragma unroll
-        for (int w = 1; w < PER; ++w) {
-            const float4 x = s_o[w * LANES + tid];
-            o.x += x.x, o.y += x.y, o.z += x.z, o.w += x.w;
+            for (int k = 0; k < AHEAD; ++k) add_part(o, y[k], exp2_approx(w[k] - m));
         }
-        store_result<D>(p, cut.y, cut.z + h, tid * 4, m, lm, l, o);
+        if (SPLIT) {
+            s_o[tid] = o;
+            __syncthreads();
+            if (group != 0) return;
+#pragma unroll
+            for (int k = 1; k < PER; ++k) add_part(o, s_o[k * LANES + tid], 1.f);
+        }
+        store_result<D>(p, cut.z, head0 + h, l4 * 4, m, lm, l, o);
     }
 }
 
