@@ -117,11 +117,7 @@ spava_status launch_rows(RowParams &p, int d, cudaStream_t st) {
     p.heads = FastDiv::of(static_cast<uint32_t>(heads));
     const uint32_t per_block = kRowThreads / (d / 16);
     const unsigned grid = (p.n_items + per_block - 1) / per_block;
-    if (d == 64)
-        row_kernel<64, CACHE><<<grid, kRowThreads, 0, st>>>(p);
-    else
-        row_kernel<128, CACHE><<<grid, kRowThreads, 0, st>>>(p);
-    return launched();
+    return launch(d == 64 ? row_kernel<64, CACHE> : row_kernel<128, CACHE>, grid, kRowThreads, 0, 1, st, p);
 }
 
 spava_status set_rope(const spava_rope_config *c, RowParams *p, const void *q_weight,
@@ -180,37 +176,23 @@ spava_status launch_decode(DecodeParams &p, int64_t max_units, cudaStream_t st) 
     int dev = 0, n_sm = 0;
     SPAVA_CUDA(cudaGetDevice(&dev));
     SPAVA_CUDA(cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev));
-    cudaLaunchAttribute attr{};
-    cudaLaunchConfig_t cfg{};
-    cfg.blockDim = dim3(kDecThreads);
-    cfg.stream = st;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
     const int64_t items = int64_t(p.cache.n_seqs) * p.cache.Hkv * p.n_hg;
     p.cluster = kDecCluster;
     while (p.cluster > 1 && items * p.cluster > 2 * n_sm) p.cluster /= 2;
     if (items * p.cluster <= 2 * n_sm && int64_t(p.cache.cap) * 2 * S::ROW <= kClusterBlockBytes * p.cluster) {
         SPAVA_TRY(set_dynamic_smem(decode_cluster_kernel<D, E4M3, NT>, S::SMEM, cluster_done, dev));
-        attr.id = cudaLaunchAttributeClusterDimension;
-        attr.val.clusterDim.x = p.cluster;
-        attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-        cfg.gridDim = dim3(static_cast<unsigned>(items * p.cluster));
-        cfg.dynamicSmemBytes = S::SMEM;
-        return cuda_ok(cudaLaunchKernelEx(&cfg, decode_cluster_kernel<D, E4M3, NT>, p));
+        return launch(decode_cluster_kernel<D, E4M3, NT>, static_cast<unsigned>(items * p.cluster), kDecThreads,
+                      S::SMEM, p.cluster, st, p);
     }
     SPAVA_TRY(set_dynamic_smem(decode_kernel<D, E4M3, NT>, S::SMEM, done, dev));
     // no more blocks than the units of full tables
     const int grid = static_cast<int>(std::min<int64_t>(std::min(2 * n_sm, kDecMaxCtas), max_units));
     p.cuts_by_item = items <= grid;
-    decode_kernel<D, E4M3, NT><<<grid, kDecThreads, S::SMEM, st>>>(p);
-    SPAVA_TRY(launched());
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
+    SPAVA_TRY(launch(decode_kernel<D, E4M3, NT>, grid, kDecThreads, S::SMEM, 1, st, p));
     const int cuts = static_cast<int>(std::min<int64_t>(items, grid));
     const bool split = cuts * 8 * NT <= grid;
-    cfg.gridDim = dim3(split ? cuts * 8 * NT : cuts);
-    return cuda_ok(split ? cudaLaunchKernelEx(&cfg, join_kernel<D, NT, true>, p)
-                         : cudaLaunchKernelEx(&cfg, join_kernel<D, NT, false>, p));
+    return launch(split ? join_kernel<D, NT, true> : join_kernel<D, NT, false>, split ? cuts * 8 * NT : cuts,
+                  kDecThreads, 0, 1, st, p);
 }
 
 }  // namespace
@@ -330,14 +312,9 @@ spava_status spava_cache_read(const spava_cache_config *cfg, const spava_cache_p
     const bool e4m3 = cfg->type == SPAVA_CACHE_E4M3;
     const uint32_t per_block = kRowThreads / (cfg->head_dim * (e4m3 ? 1 : 2) / 16);
     const unsigned grid = (p.n_items + per_block - 1) / per_block;
-    if (cfg->head_dim == 64) {
-        if (e4m3) read_kernel<64, true><<<grid, kRowThreads, 0, st>>>(p);
-        else read_kernel<64, false><<<grid, kRowThreads, 0, st>>>(p);
-    } else {
-        if (e4m3) read_kernel<128, true><<<grid, kRowThreads, 0, st>>>(p);
-        else read_kernel<128, false><<<grid, kRowThreads, 0, st>>>(p);
-    }
-    return launched();
+    void (*const kernels[4])(ReadParams) = {read_kernel<64, false>, read_kernel<64, true>,
+                                            read_kernel<128, false>, read_kernel<128, true>};
+    return launch(kernels[(cfg->head_dim == 128 ? 2 : 0) + (e4m3 ? 1 : 0)], grid, kRowThreads, 0, 1, st, p);
 }
 
 spava_status spava_cache_attn(const spava_cache_config *cfg, const spava_cache_pools *pools,

@@ -54,7 +54,7 @@ struct CacheView {
 // The tokens of sequence b, made to fit the table; out-of-range lengths are
 // reported in the status word.
 __device__ __forceinline__ int cache_len(const CacheView &c, int b) {
-    const int n = __ldg(c.lens + b);
+    const int n = c.lens[b];
     if (n < 0 || n > c.cap) {
         atomicOr(c.status, kStatusBadBatch);
         return n < 0 ? 0 : c.cap;
@@ -67,12 +67,45 @@ __device__ __forceinline__ int cache_len(const CacheView &c, int b) {
 __device__ __forceinline__ uint32_t cache_row(const CacheView &c, int b, int pos) {
     uint32_t off;
     const uint32_t at = c.page.quot(static_cast<uint32_t>(pos), off);
-    const int page = __ldg(c.table + b * c.max_pages + at);
+    const int page = c.table[b * c.max_pages + at];
     if (static_cast<uint32_t>(page) >= c.n_pages) {
         atomicOr(c.status, kStatusBadBatch);
         return kNoRow;
     }
     return static_cast<uint32_t>(page) * c.Hkv * c.page.d + off;
+}
+
+// ------------------------------------------------------------------ dependent launches
+// Every kernel here is launched as a programmatic dependent of the stream's last
+// one: it may come onto the SMs before that has ended, and touches no memory
+// before wait_for_primary, which every thread passes and which returns when all
+// work before has ended and is visible.  launch_dependents lets the next kernel
+// do the same: a decode step is a chain of launches of a few microseconds.  No
+// load goes by ld.global.nc: what the kernel before still writes is not
+// read-only for this one's whole life.
+__device__ __forceinline__ void launch_dependents() {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+__device__ __forceinline__ void wait_for_primary() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+template <typename P>
+inline spava_status launch(void (*kernel)(P), unsigned grid, unsigned threads, int smem, int cluster,
+                           cudaStream_t st, const P &p) {
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cuda_ok(cudaLaunchKernelEx(&cfg, kernel, p));
 }
 
 // ------------------------------------------------------------------ e4m3

@@ -33,15 +33,6 @@ struct DecodeParams {
     float *part_o;        // [2 * kDecMaxCtas][8 * NT][D]
 };
 
-// Programmatic dependent launch: the join's blocks are on the SMs, waiting,
-// while the parts are computed.
-__device__ __forceinline__ void launch_dependents() {
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
-__device__ __forceinline__ void wait_for_primary() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(bytes)
@@ -222,6 +213,8 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
     const int g = lane / 4, c = lane % 4;
     const CacheView &cv = p.cache;
     const int per_seq = cv.Hkv * p.n_hg;  // items (KV head, head group) of a sequence
+    launch_dependents();
+    wait_for_primary();
 
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) +
                           warp * (kDecStages * kDecTileBytes);
@@ -249,7 +242,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
                 // 16 bytes of q: eight elements, from 8 (c + 4 j) on (bf16), or
                 // half of the sixteen from 16 (c + 4 (j / 2)) on (e4m3)
                 const int e0 = E4M3 ? 16 * (c + 4 * (j / 2)) + 8 * (j % 2) : 8 * (c + 4 * j);
-                const uint4 x = h < n_heads ? __ldg(reinterpret_cast<const uint4 *>(src + e0))
+                const uint4 x = h < n_heads ? *reinterpret_cast<const uint4 *>(src + e0)
                                             : make_uint4(0, 0, 0, 0);
                 w[2 * j][0] = x.x, w[2 * j][1] = x.y, w[2 * j + 1][0] = x.z, w[2 * j + 1][1] = x.w;
             }
@@ -351,7 +344,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
 #pragma unroll
                 for (int k = 0; k < RW; ++k) {
                     const int64_t t = token(i, k);
-                    page[i][k] = held_token(i, t) ? __ldg(table + cv.page.quot(static_cast<uint32_t>(t))) : 0;
+                    page[i][k] = held_token(i, t) ? table[cv.page.quot(static_cast<uint32_t>(t))] : 0;
                 }
 #pragma unroll
             for (int i = 0; i < K; ++i) {
@@ -625,8 +618,6 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
     if constexpr (!CLUSTER) {
         __shared__ int s_prefix[kDecThreads + 1];
         __shared__ int s_warp[kDecWarps];
-        launch_dependents();
-    
         // ---- the line of units: sequence groups of `per`, s_prefix[i] the unit where group i begins
         int per, total;
         bool empty;  // there are sequences without positions
@@ -666,7 +657,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
             total = s_prefix[kDecThreads];
             empty = true;
         }
-    
+
         // ---- sequences without positions
         if (empty)
             for (int b = blockIdx.x; b < cv.n_seqs; b += gridDim.x) {
@@ -679,7 +670,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
                 if (p.cuts_by_item)
                     for (int i = tid; i < per_seq; i += kDecThreads) p.cuts[b * per_seq + i] = make_int4(0, 0, 0, 0);
             }
-    
+
         // Shares of `base` units, of one more for the first `more` blocks.
         const int ctas = min(total, static_cast<int>(gridDim.x));  // blocks with a share
         const int cta = blockIdx.x;
@@ -692,7 +683,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
             const int y = x - more * (base + 1);
             return y < 0 ? x / (base + 1) : more + y / base;
         };
-    
+
         // ---- the sequence of the first unit
         int b, first;  // first: the unit where sequence b begins
         {
@@ -829,6 +820,7 @@ __global__ void __launch_bounds__(kDecThreads) join_kernel(const __grid_constant
     constexpr int AHEAD = SPLIT ? 8 : 4;
     __shared__ float4 s_o[kDecThreads];
     const int tid = threadIdx.x, l4 = tid % LANES, group = tid / LANES;
+    launch_dependents();
     wait_for_primary();
     const int4 cut = __ldcg(p.cuts + (SPLIT ? blockIdx.x / HEADS : blockIdx.x));
     const int c0 = cut.x, parts = cut.y;

@@ -94,6 +94,8 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
     constexpr int TOK = ITEMS / 2 + 1;
     __shared__ __align__(16) float s_cos[TOK * (D / 2)], s_sin[TOK * (D / 2)];
 
+    launch_dependents();
+    wait_for_primary();
     const uint32_t item0 = blockIdx.x * static_cast<uint32_t>(ITEMS);
     const uint32_t item = item0 + threadIdx.x / L;
     const int l = threadIdx.x % L;
@@ -145,9 +147,9 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
         for (int i = threadIdx.x; i < n; i += kRowThreads) {
             const int t = i / half, j = i - t * half;
             const int axis = (j >= p.cut1) + (j >= p.cut2) + (j >= p.cut3);
-            const int pos = __ldg(p.positions + axis * p.n_rows + tok0 + t);
+            const int pos = p.positions[axis * p.n_rows + tok0 + t];
             const double a = static_cast<double>(pos) *
-                             (static_cast<double>(__ldg(p.inv_freq + j)) * 0.15915494309189533577);
+                             (static_cast<double>(p.inv_freq[j]) * 0.15915494309189533577);
             const float r = static_cast<float>(a - rint(a));
             float sn, cs;
             sincospif(2.f * r, &sn, &cs);
@@ -171,8 +173,8 @@ __global__ void __launch_bounds__(kRowThreads) row_kernel(const __grid_constant_
             const __nv_bfloat16 *wt = kind == 0 ? p.q_weight : p.k_weight;
             if (wt) {
                 float g0[8], g1[8];
-                unpack8(__ldg(reinterpret_cast<const uint4 *>(wt + c0 * 8)), g0);
-                unpack8(__ldg(reinterpret_cast<const uint4 *>(wt + c1 * 8)), g1);
+                unpack8(*reinterpret_cast<const uint4 *>(wt + c0 * 8), g0);
+                unpack8(*reinterpret_cast<const uint4 *>(wt + c1 * 8), g1);
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x0[i] = x0[i] * r * g0[i], x1[i] = x1[i] * r * g1[i];
             } else {
@@ -259,6 +261,8 @@ template <int D, bool E4M3>
 __global__ void __launch_bounds__(kRowThreads) read_kernel(const __grid_constant__ ReadParams p) {
     constexpr int L = D * (E4M3 ? 1 : 2) / 16;
     constexpr int ITEMS = kRowThreads / L;
+    launch_dependents();
+    wait_for_primary();
     const uint32_t item = blockIdx.x * static_cast<uint32_t>(ITEMS) + threadIdx.x / L;
     if (item >= p.n_items) return;
     const int l = threadIdx.x % L;
