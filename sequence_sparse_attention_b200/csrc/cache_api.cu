@@ -108,16 +108,29 @@ spava_status make_view(const spava_cache_config *c, const spava_cache_pools *p,
     return SPAVA_OK;
 }
 
-template <int CACHE>
+// Tokens of a block (a power of two up to `most`) and blocks that share their
+// items: few tokens are spread over the SMs head by head, many share what a
+// block makes for them.  per_pass: items a block works on at a time.
+void split_tokens(int64_t n_rows, int64_t heads, int most, int per_pass, int32_t *tokens_log2, int64_t *splits) {
+    constexpr int kBlocks = 148 * 4;  // enough to fill the SMs
+    int lg = 0;
+    while ((2 << lg) <= most && (n_rows >> (lg + 1)) >= kBlocks) ++lg;
+    const int64_t groups = (n_rows + (1LL << lg) - 1) >> lg, passes = ((heads << lg) + per_pass - 1) / per_pass;
+    *tokens_log2 = lg;
+    *splits = std::max<int64_t>(1, std::min(passes, kBlocks / groups));
+}
+
+template <int CACHE, bool ROPE>
 spava_status launch_rows(RowParams &p, int d, cudaStream_t st) {
     const int64_t heads = int64_t(p.Hq) + p.Hk + p.Hv;
     if (p.n_rows == 0) return SPAVA_OK;
     if (p.n_rows >= (1LL << 31) / heads) return SPAVA_ERR_UNSUPPORTED;
-    p.n_items = static_cast<uint32_t>(p.n_rows * heads);
-    p.heads = FastDiv::of(static_cast<uint32_t>(heads));
-    const uint32_t per_block = kRowThreads / (d / 16);
-    const unsigned grid = (p.n_items + per_block - 1) / per_block;
-    return launch(d == 64 ? row_kernel<64, CACHE> : row_kernel<128, CACHE>, grid, kRowThreads, 0, 1, st, p);
+    int64_t splits;
+    split_tokens(p.n_rows, heads, kRowTokens, kRowThreads / (d / 16), &p.tokens_log2, &splits);
+    p.splits = FastDiv::of(static_cast<uint32_t>(splits));
+    const int64_t groups = (p.n_rows + (1LL << p.tokens_log2) - 1) >> p.tokens_log2;
+    return launch(d == 64 ? row_kernel<64, CACHE, ROPE> : row_kernel<128, CACHE, ROPE>,
+                  static_cast<unsigned>(groups * splits), kRowThreads, 0, 1, st, p);
 }
 
 spava_status set_rope(const spava_rope_config *c, RowParams *p, const void *q_weight,
@@ -221,7 +234,7 @@ spava_status spava_qk_norm_rope(const spava_rope_config *cfg, int64_t n_rows, co
     p.n_rows = n_rows;
     p.Hq = cfg->n_q_heads;
     p.Hk = cfg->n_kv_heads;
-    return launch_rows<0>(p, cfg->head_dim, static_cast<cudaStream_t>(stream));
+    return launch_rows<0, true>(p, cfg->head_dim, static_cast<cudaStream_t>(stream));
 }
 
 spava_status spava_cache_workspace_size(const spava_cache_config *cfg, size_t *bytes) {
@@ -249,8 +262,8 @@ spava_status spava_cache_write(const spava_cache_config *cfg, const spava_cache_
     p.new_rows = FastDiv::of(static_cast<uint32_t>(new_rows));
     p.Hk = p.Hv = cfg->n_kv_heads;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return cfg->type == SPAVA_CACHE_E4M3 ? launch_rows<2>(p, cfg->head_dim, st)
-                                         : launch_rows<1>(p, cfg->head_dim, st);
+    return cfg->type == SPAVA_CACHE_E4M3 ? launch_rows<2, false>(p, cfg->head_dim, st)
+                                         : launch_rows<1, false>(p, cfg->head_dim, st);
 }
 
 spava_status spava_cache_append(const spava_rope_config *rope, const spava_cache_config *cfg,
@@ -285,8 +298,8 @@ spava_status spava_cache_append(const spava_rope_config *rope, const spava_cache
     p.Hq = cfg->n_q_heads;
     p.Hk = p.Hv = cfg->n_kv_heads;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    return cfg->type == SPAVA_CACHE_E4M3 ? launch_rows<2>(p, cfg->head_dim, st)
-                                         : launch_rows<1>(p, cfg->head_dim, st);
+    return cfg->type == SPAVA_CACHE_E4M3 ? launch_rows<2, true>(p, cfg->head_dim, st)
+                                         : launch_rows<1, true>(p, cfg->head_dim, st);
 }
 
 spava_status spava_cache_read(const spava_cache_config *cfg, const spava_cache_pools *pools,
@@ -305,13 +318,15 @@ spava_status spava_cache_read(const spava_cache_config *cfg, const spava_cache_p
     p.k_out = static_cast<__nv_bfloat16 *>(k_out);
     p.v_out = static_cast<__nv_bfloat16 *>(v_out);
     p.first = static_cast<int32_t>(first);
-    p.n_items = static_cast<uint32_t>(batch->n_seqs * rows * heads);
+    p.n_rows = batch->n_seqs * rows;
     p.rows = FastDiv::of(static_cast<uint32_t>(rows));
     p.heads = FastDiv::of(static_cast<uint32_t>(heads));
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool e4m3 = cfg->type == SPAVA_CACHE_E4M3;
-    const uint32_t per_block = kRowThreads / (cfg->head_dim * (e4m3 ? 1 : 2) / 16);
-    const unsigned grid = (p.n_items + per_block - 1) / per_block;
+    int64_t splits;
+    split_tokens(p.n_rows, heads, kReadTokens, kRowThreads / (cfg->head_dim / 8), &p.tokens_log2, &splits);
+    p.splits = FastDiv::of(static_cast<uint32_t>(splits));
+    const unsigned grid = static_cast<unsigned>(((p.n_rows + (1LL << p.tokens_log2) - 1) >> p.tokens_log2) * splits);
     void (*const kernels[4])(ReadParams) = {read_kernel<64, false>, read_kernel<64, true>,
                                             read_kernel<128, false>, read_kernel<128, true>};
     return launch(kernels[(cfg->head_dim == 128 ? 2 : 0) + (e4m3 ? 1 : 0)], grid, kRowThreads, 0, 1, st, p);
