@@ -1,0 +1,376 @@
+// calls.cpp -- the Python side of the answering calls (include/spava.h): checks
+// of tensors, outputs, the current stream, and the library call, compiled.  A
+// decode step makes these calls many thousand times a second on tensors of a few
+// KiB; interpreted (ctypes, one attribute at a time) the host's part of a call is
+// 6 to 9 us beside a launch's 2.5, here it is about one.
+//
+// Argument marshalling only, like api.py: the computation is libspava's.
+#define PY_SSIZE_T_CLEAN
+#include <Python.h>
+
+#include <ATen/ATen.h>
+#include <c10/cuda/CUDAGuard.h>
+#include <c10/cuda/CUDAStream.h>
+#include <torch/csrc/Exceptions.h>
+#include <torch/csrc/autograd/python_variable.h>
+
+#include <string>
+
+#include "../../include/spava.h"
+
+namespace {
+
+// ------------------------------------------------------------------ checks
+struct Refused {  // becomes a ValueError
+    std::string what;
+};
+
+std::string said(const at::Tensor &t) {
+    return c10::str(t.scalar_type(), " ", t.sizes(), " on ", t.device(), " strides ", t.strides());
+}
+
+const at::Tensor &tensor(PyObject *o, const char *name) {
+    if (!THPVariable_Check(o)) throw Refused{c10::str(name, ": expected a tensor, got ", Py_TYPE(o)->tp_name)};
+    return THPVariable_Unpack(o);
+}
+
+bool on(const at::Tensor &t, int index) { return t.is_cuda() && t.get_device() == index; }
+
+void check(const at::Tensor &t, at::IntArrayRef shape, at::ScalarType type, int index, const char *name) {
+    if (t.scalar_type() != type || t.sizes() != shape || !on(t, index) || !t.is_contiguous())
+        throw Refused{c10::str(name, ": expected contiguous ", type, " ", shape, " on cuda:", index, ", got ", said(t))};
+}
+
+// Elements between the tokens of a bf16 [rows, heads, d] tensor or view.
+int64_t token_stride(const at::Tensor &t, int64_t rows, int64_t heads, int64_t d, int index, const char *name) {
+    if (t.scalar_type() != at::kBFloat16 || t.dim() != 3 || t.size(0) != rows || t.size(1) != heads ||
+        t.size(2) != d || !on(t, index))
+        throw Refused{c10::str(name, ": expected BFloat16 [", rows, ", ", heads, ", ", d, "] on cuda:", index, ", got ",
+                               said(t))};
+    if (t.stride(2) != 1 || (heads > 1 && t.stride(1) != d))
+        throw Refused{c10::str(name, ": the heads of a token must be contiguous, got ", said(t))};
+    return rows > 1 ? t.stride(0) : heads * d;
+}
+
+int64_t rows_of(const at::Tensor &t, const char *name) {
+    if (t.dim() != 3) throw Refused{c10::str(name, ": expected [rows, heads, d], got ", said(t))};
+    return t.size(0);
+}
+
+int64_t new_rows_of(int64_t rows, int64_t n_seqs, const char *name) {
+    if (rows == 0 && n_seqs == 0) return 0;
+    if (n_seqs == 0 || rows % n_seqs)
+        throw Refused{c10::str(name, ": ", rows, " rows for ", n_seqs, " sequences: expected as many for each")};
+    return rows / n_seqs;
+}
+
+// The given output, checked, or a new one.
+at::Tensor output(PyObject *given, at::IntArrayRef shape, at::ScalarType type, int index, const char *name) {
+    if (given != Py_None) {
+        const at::Tensor &t = tensor(given, name);
+        check(t, shape, type, index, name);
+        return t;
+    }
+    return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, index)));
+}
+
+void *ptr(const at::Tensor &t) { return t.data_ptr(); }
+
+// ------------------------------------------------------------------ calls
+PyObject *g_failed = nullptr;  // (function name, status): raises
+
+template <typename F>
+bool called(const char *name, int index, F f) {
+    spava_status rc;
+    {
+        c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
+        void *stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream();
+        Py_BEGIN_ALLOW_THREADS;
+        rc = f(stream);
+        Py_END_ALLOW_THREADS;
+    }
+    if (rc == SPAVA_OK) return true;
+    if (!g_failed) {
+        PyErr_Format(PyExc_RuntimeError, "%s: status %d", name, int(rc));
+    } else if (PyObject *r = PyObject_CallFunction(g_failed, "si", name, int(rc))) {
+        Py_DECREF(r);
+        PyErr_Format(PyExc_RuntimeError, "%s: status %d", name, int(rc));
+    }
+    return false;
+}
+
+template <typename F>
+PyObject *guarded(F f) {
+    HANDLE_TH_ERRORS
+    try {
+        return f();
+    } catch (const Refused &r) {
+        PyErr_SetString(PyExc_ValueError, r.what.c_str());
+        return nullptr;
+    }
+    END_HANDLE_TH_ERRORS
+}
+
+bool arguments(Py_ssize_t n, Py_ssize_t want, const char *name) {
+    if (n == want) return true;
+    PyErr_Format(PyExc_TypeError, "%s: expected %zd arguments, got %zd", name, want, n);
+    return false;
+}
+
+PyObject *pair(const at::Tensor &a, PyObject *b) {  // steals b
+    PyObject *x = THPVariable_Wrap(a);
+    if (!x || !b) {
+        Py_XDECREF(x);
+        Py_XDECREF(b);
+        return nullptr;
+    }
+    PyObject *t = PyTuple_New(2);
+    if (!t) {
+        Py_DECREF(x);
+        Py_DECREF(b);
+        return nullptr;
+    }
+    PyTuple_SET_ITEM(t, 0, x);
+    PyTuple_SET_ITEM(t, 1, b);
+    return t;
+}
+
+// ------------------------------------------------------------------ Rope
+// The tables' memory is the Python object's, which holds this one.
+struct Rope {
+    PyObject_HEAD
+    spava_rope_config cfg;
+    const void *q_weight, *k_weight;
+    const float *inv_freq;
+    int index;
+};
+
+// (address of a spava_rope_config, q_weight, k_weight, inv_freq addresses, device)
+int rope_init(PyObject *self, PyObject *args, PyObject *) {
+    Rope *r = reinterpret_cast<Rope *>(self);
+    unsigned long long cfg, q, k, f;
+    if (!PyArg_ParseTuple(args, "KKKKi", &cfg, &q, &k, &f, &r->index)) return -1;
+    r->cfg = *reinterpret_cast<const spava_rope_config *>(cfg);
+    r->q_weight = reinterpret_cast<const void *>(q);
+    r->k_weight = reinterpret_cast<const void *>(k);
+    r->inv_freq = reinterpret_cast<const float *>(f);
+    return 0;
+}
+
+const int32_t *positions_of(const Rope *r, PyObject *o, int64_t rows) {
+    if (r->cfg.rope_dim == 0) return nullptr;
+    if (o == Py_None) throw Refused{"positions: a rotation needs them"};
+    const at::Tensor &t = tensor(o, "positions");
+    const int64_t axes = r->cfg.n_axes;
+    const bool shaped = t.dim() == 2 ? t.size(0) == axes && t.size(1) == rows : axes == 1 && t.dim() == 1 && t.size(0) == rows;
+    if (t.scalar_type() != at::kInt || !shaped || !on(t, r->index) || !t.is_contiguous())
+        throw Refused{c10::str("positions: expected contiguous Int [", axes, ", ", rows, "] on cuda:", r->index, ", got ",
+                               said(t))};
+    return static_cast<const int32_t *>(ptr(t));
+}
+
+// apply(q, k, positions, q_out, k_out)
+PyObject *rope_apply(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    if (!arguments(n, 5, "apply")) return nullptr;
+    return guarded([&]() -> PyObject * {
+        const Rope *r = reinterpret_cast<Rope *>(self);
+        const spava_rope_config &c = r->cfg;
+        const at::Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
+        const int64_t rows = rows_of(q, "q");
+        const int64_t qs = token_stride(q, rows, c.n_q_heads, c.head_dim, r->index, "q");
+        const int64_t ks = token_stride(k, rows, c.n_kv_heads, c.head_dim, r->index, "k");
+        const int32_t *pos = positions_of(r, a[2], rows);
+        const at::Tensor qo = output(a[3], q.sizes(), at::kBFloat16, r->index, "q_out");
+        const at::Tensor ko = output(a[4], k.sizes(), at::kBFloat16, r->index, "k_out");
+        if (!called("spava_qk_norm_rope", r->index, [&](void *stream) {
+                return spava_qk_norm_rope(&c, rows, ptr(q), qs, ptr(k), ks, r->q_weight, r->k_weight, r->inv_freq, pos,
+                                          ptr(qo), ptr(ko), stream);
+            }))
+            return nullptr;
+        return pair(qo, THPVariable_Wrap(ko));
+    });
+}
+
+PyMethodDef rope_methods[] = {
+    {"apply", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(rope_apply)), METH_FASTCALL, nullptr},
+    {nullptr, nullptr, 0, nullptr}};
+
+PyTypeObject RopeType = {PyVarObject_HEAD_INIT(nullptr, 0)};
+
+// ------------------------------------------------------------------ Cache
+struct Cache {
+    PyObject_HEAD
+    spava_cache_config cfg;
+    spava_cache_pools pools;
+    void *ws;
+    unsigned long long ws_bytes;
+    int index;
+};
+
+// (addresses of a spava_cache_config and a spava_cache_pools, of the workspace,
+// its bytes, device)
+int cache_init(PyObject *self, PyObject *args, PyObject *) {
+    Cache *c = reinterpret_cast<Cache *>(self);
+    unsigned long long cfg, pools, ws;
+    if (!PyArg_ParseTuple(args, "KKKKi", &cfg, &pools, &ws, &c->ws_bytes, &c->index)) return -1;
+    c->cfg = *reinterpret_cast<const spava_cache_config *>(cfg);
+    c->pools = *reinterpret_cast<const spava_cache_pools *>(pools);
+    c->ws = reinterpret_cast<void *>(ws);
+    return 0;
+}
+
+struct Space {
+    void *ws;
+    size_t bytes;
+};
+Space space_of(const Cache *c, PyObject *given) {
+    if (given == Py_None) return {c->ws, static_cast<size_t>(c->ws_bytes)};
+    const at::Tensor &t = tensor(given, "workspace");
+    if (t.scalar_type() != at::kByte || !on(t, c->index) || !t.is_contiguous())
+        throw Refused{c10::str("workspace: expected contiguous Byte on cuda:", c->index, ", got ", said(t))};
+    return {ptr(t), static_cast<size_t>(t.numel())};
+}
+
+spava_cache_batch batch_of(const Cache *c, PyObject *table, PyObject *lens) {
+    const at::Tensor &t = tensor(table, "table"), &l = tensor(lens, "lens");
+    if (t.scalar_type() != at::kInt || l.scalar_type() != at::kInt || t.dim() != 2 || l.dim() != 1 ||
+        t.size(0) != l.size(0) || !on(t, c->index) || !on(l, c->index) || !t.is_contiguous() || !l.is_contiguous())
+        throw Refused{c10::str("table, lens: expected contiguous Int [sequences, max_pages] and [sequences] on cuda:",
+                               c->index, ", got ", said(t), " and ", said(l))};
+    return {t.size(0), t.size(1), static_cast<const int32_t *>(ptr(t)), static_cast<const int32_t *>(ptr(l))};
+}
+
+// write(k, v, table, lens, workspace)
+PyObject *cache_write(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    if (!arguments(n, 5, "write")) return nullptr;
+    return guarded([&]() -> PyObject * {
+        const Cache *c = reinterpret_cast<Cache *>(self);
+        const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
+        const spava_cache_batch batch = batch_of(c, a[2], a[3]);
+        const int64_t rows = rows_of(k, "k"), fresh = new_rows_of(rows, batch.n_seqs, "k");
+        const int64_t ks = token_stride(k, rows, c->cfg.n_kv_heads, c->cfg.head_dim, c->index, "k");
+        const int64_t vs = token_stride(v, rows, c->cfg.n_kv_heads, c->cfg.head_dim, c->index, "v");
+        const Space s = space_of(c, a[4]);
+        if (!called("spava_cache_write", c->index, [&](void *stream) {
+                return spava_cache_write(&c->cfg, &c->pools, &batch, fresh, ptr(k), ks, ptr(v), vs, s.ws, s.bytes, stream);
+            }))
+            return nullptr;
+        Py_RETURN_NONE;
+    });
+}
+
+// append(rope, q, k, v, positions, table, lens, q_out, workspace)
+PyObject *cache_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    if (!arguments(n, 9, "append")) return nullptr;
+    return guarded([&]() -> PyObject * {
+        const Cache *c = reinterpret_cast<Cache *>(self);
+        if (!PyObject_TypeCheck(a[0], &RopeType)) throw Refused{"rope: expected a QKNormRope"};
+        const Rope *r = reinterpret_cast<Rope *>(a[0]);
+        if (r->index != c->index)
+            throw Refused{c10::str("rope: expected on cuda:", c->index, ", is on cuda:", r->index)};
+        const at::Tensor &q = tensor(a[1], "q"), &k = tensor(a[2], "k"), &v = tensor(a[3], "v");
+        const spava_cache_batch batch = batch_of(c, a[5], a[6]);
+        const int64_t rows = rows_of(q, "q"), fresh = new_rows_of(rows, batch.n_seqs, "q");
+        const int64_t qs = token_stride(q, rows, c->cfg.n_q_heads, c->cfg.head_dim, c->index, "q");
+        const int64_t ks = token_stride(k, rows, c->cfg.n_kv_heads, c->cfg.head_dim, c->index, "k");
+        const int64_t vs = token_stride(v, rows, c->cfg.n_kv_heads, c->cfg.head_dim, c->index, "v");
+        const int32_t *pos = positions_of(r, a[4], rows);
+        const Space s = space_of(c, a[8]);
+        const at::Tensor qo = output(a[7], q.sizes(), at::kBFloat16, c->index, "q_out");
+        if (!called("spava_cache_append", c->index, [&](void *stream) {
+                return spava_cache_append(&r->cfg, &c->cfg, &c->pools, &batch, fresh, ptr(q), qs, ptr(k), ks, ptr(v), vs,
+                                          r->q_weight, r->k_weight, r->inv_freq, pos, ptr(qo), s.ws, s.bytes, stream);
+            }))
+            return nullptr;
+        return THPVariable_Wrap(qo);
+    });
+}
+
+// read(table, lens, rows, first, k_out, v_out, workspace)
+PyObject *cache_read(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    if (!arguments(n, 7, "read")) return nullptr;
+    return guarded([&]() -> PyObject * {
+        const Cache *c = reinterpret_cast<Cache *>(self);
+        const spava_cache_batch batch = batch_of(c, a[0], a[1]);
+        const int64_t rows = PyLong_AsLongLong(a[2]), first = PyLong_AsLongLong(a[3]);
+        if (PyErr_Occurred()) return nullptr;
+        if (rows < 0 || first < 0) throw Refused{c10::str("rows, first: expected >= 0, got ", rows, " and ", first)};
+        const int64_t shape[4] = {batch.n_seqs, rows, c->cfg.n_kv_heads, c->cfg.head_dim};
+        const Space s = space_of(c, a[6]);
+        const at::Tensor ko = output(a[4], shape, at::kBFloat16, c->index, "k_out");
+        const at::Tensor vo = output(a[5], shape, at::kBFloat16, c->index, "v_out");
+        if (!called("spava_cache_read", c->index, [&](void *stream) {
+                return spava_cache_read(&c->cfg, &c->pools, &batch, first, rows, ptr(ko), ptr(vo), s.ws, s.bytes, stream);
+            }))
+            return nullptr;
+        return pair(ko, THPVariable_Wrap(vo));
+    });
+}
+
+// attn(q, table, lens, o, lse, want_lse, workspace)
+PyObject *cache_attn(PyObject *self, PyObject *const *a, Py_ssize_t n) {
+    if (!arguments(n, 7, "attn")) return nullptr;
+    return guarded([&]() -> PyObject * {
+        const Cache *c = reinterpret_cast<Cache *>(self);
+        const at::Tensor &q = tensor(a[0], "q");
+        const spava_cache_batch batch = batch_of(c, a[1], a[2]);
+        const int64_t shape[3] = {batch.n_seqs, c->cfg.n_q_heads, c->cfg.head_dim};
+        check(q, shape, at::kBFloat16, c->index, "q");
+        const Space s = space_of(c, a[6]);
+        const at::Tensor o = output(a[3], shape, at::kBFloat16, c->index, "o");
+        const int64_t lse_shape[2] = {c->cfg.n_q_heads, batch.n_seqs};
+        const int want = PyObject_IsTrue(a[5]);
+        if (want < 0) return nullptr;
+        at::Tensor lse;
+        if (want || a[4] != Py_None) lse = output(a[4], lse_shape, at::kFloat, c->index, "lse");
+        if (!called("spava_cache_attn", c->index, [&](void *stream) {
+                return spava_cache_attn(&c->cfg, &c->pools, &batch, ptr(q), ptr(o),
+                                        lse.defined() ? static_cast<float *>(ptr(lse)) : nullptr, s.ws, s.bytes, stream);
+            }))
+            return nullptr;
+        return pair(o, lse.defined() ? THPVariable_Wrap(lse) : Py_NewRef(Py_None));
+    });
+}
+
+#define SPAVA_METHOD(name, f) \
+    {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)(void)>(f)), METH_FASTCALL, nullptr}
+PyMethodDef cache_methods[] = {SPAVA_METHOD("write", cache_write), SPAVA_METHOD("append", cache_append),
+                               SPAVA_METHOD("read", cache_read), SPAVA_METHOD("attn", cache_attn),
+                               {nullptr, nullptr, 0, nullptr}};
+
+PyTypeObject CacheType = {PyVarObject_HEAD_INIT(nullptr, 0)};
+
+// on_failure(f): f(function name, status) raises what a refused call raises
+PyObject *on_failure(PyObject *, PyObject *f) {
+    Py_INCREF(f);
+    Py_XSETREF(g_failed, f);
+    Py_RETURN_NONE;
+}
+
+PyMethodDef module_methods[] = {{"on_failure", on_failure, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
+PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, module_methods};
+
+int add_type(PyObject *m, PyTypeObject &t, const char *name, const char *full, Py_ssize_t size, PyMethodDef *methods,
+             initproc init) {
+    t.tp_name = full;
+    t.tp_basicsize = size;
+    t.tp_flags = Py_TPFLAGS_DEFAULT;
+    t.tp_methods = methods;
+    t.tp_init = init;
+    t.tp_new = PyType_GenericNew;
+    if (PyType_Ready(&t) < 0) return -1;
+    return PyModule_AddObjectRef(m, name, reinterpret_cast<PyObject *>(&t));
+}
+
+}  // namespace
+
+PyMODINIT_FUNC PyInit__calls() {
+    PyObject *m = PyModule_Create(&module);
+    if (!m) return nullptr;
+    if (add_type(m, RopeType, "Rope", "_calls.Rope", sizeof(Rope), rope_methods, rope_init) < 0 ||
+        add_type(m, CacheType, "Cache", "_calls.Cache", sizeof(Cache), cache_methods, cache_init) < 0) {
+        Py_DECREF(m);
+        return nullptr;
+    }
+    return m;
+}
