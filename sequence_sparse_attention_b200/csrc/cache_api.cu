@@ -203,9 +203,10 @@ spava_status launch_decode(DecodeParams &p, int64_t max_units, cudaStream_t st) 
     p.cuts_by_item = items <= grid;
     SPAVA_TRY(launch(decode_kernel<D, E4M3, NT>, grid, kDecThreads, S::SMEM, 1, st, p));
     const int cuts = static_cast<int>(std::min<int64_t>(items, grid));
-    const bool split = cuts * 8 * NT <= grid;
-    return launch(split ? join_kernel<D, NT, true> : join_kernel<D, NT, false>, split ? cuts * 8 * NT : cuts,
-                  kDecThreads, 0, 1, st, p);
+    constexpr int kSplitBlocks = 8 * NT * (D / 32);  // of an item
+    const bool split = cuts * kSplitBlocks <= 2 * grid;
+    return launch(split ? join_kernel<D, NT, true> : join_kernel<D, NT, false>, split ? cuts * kSplitBlocks : cuts,
+                  split ? kJoinThreads : kDecThreads, 0, 1, st, p);
 }
 
 }  // namespace
@@ -358,7 +359,7 @@ spava_status spava_cache_attn(const spava_cache_config *cfg, const spava_cache_p
     const bool e4m3 = cfg->type == SPAVA_CACHE_E4M3;
     // the units of a batch of full tables are counted in 32 bits
     const int64_t block = int64_t(kDecWarps) * kDecTileBytes / (2 * cfg->head_dim * (e4m3 ? 1 : 2));
-    const int64_t units = (p.cache.cap + block - 1) / block * cfg->n_kv_heads * p.n_hg;
+    const int64_t units = ((p.cache.cap + block - 1) / block + kDecItemCost) * cfg->n_kv_heads * p.n_hg;
     if (units >= (1LL << 31) / batch->n_seqs) return SPAVA_ERR_UNSUPPORTED;
     const int64_t all = units * batch->n_seqs;
     if (cfg->head_dim == 64) {

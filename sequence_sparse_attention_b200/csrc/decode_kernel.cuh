@@ -8,8 +8,13 @@ namespace spava {
 
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kJoinThreads = 256;  // of a join block that shares its parts out
 constexpr int kDecCluster = 8;    // most blocks of decode_cluster_kernel's clusters
 constexpr int kDecMaxCtas = 320;  // the workspace's partials are sized for these
+// Beginning and ending an item takes a block about as long as two units of its
+// tokens, and counts as that: 17 sequences of 100 to 16100 tokens take 55 us, 70
+// where only tokens count and some block gets the many short items (e4m3, 8 KV heads).
+constexpr int kDecItemCost = 2;
 constexpr int kDecStages = 3;
 constexpr int kDecTileBytes = 8192;  // K and V bytes of one warp's tile
 constexpr int kDecRingBytes = kDecWarps * kDecStages * kDecTileBytes;
@@ -29,7 +34,7 @@ struct DecodeParams {
     // parts: not cut.  And its sequence and head group.
     int4 *cuts;
     int32_t cuts_by_item;
-    float *part_stat;     // [2 * kDecMaxCtas][3][8 * NT]
+    float *part_stat;     // [8 * NT][3][2][kDecMaxCtas]: m, lm, l of a block's first and second part
     float *part_o;        // [2 * kDecMaxCtas][8 * NT][D]
 };
 
@@ -616,6 +621,8 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
         }
     };
     if constexpr (!CLUSTER) {
+        // units of the line that an item takes
+        auto item_cost = [](int len) { return len > 0 ? (len + S::BLOCK - 1) / S::BLOCK + kDecItemCost : 0; };
         __shared__ int s_prefix[kDecThreads + 1];
         __shared__ int s_warp[kDecWarps];
         // ---- the line of units: sequence groups of `per`, s_prefix[i] the unit where group i begins
@@ -626,7 +633,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
             per = 1;
             const int len = lane < cv.n_seqs ? cache_len(cv, lane) : 1;
             empty = __any_sync(0xffffffffu, len == 0);
-            int scan = lane < cv.n_seqs ? (len + S::BLOCK - 1) / S::BLOCK * per_seq : 0;
+            int scan = lane < cv.n_seqs ? item_cost(len) * per_seq : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, scan, o);
@@ -640,7 +647,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
             per = (cv.n_seqs + kDecThreads - 1) / kDecThreads;
             int scan = 0;
             for (int b = tid * per; b < min((tid + 1) * per, cv.n_seqs); ++b)
-                scan += (cache_len(cv, b) + S::BLOCK - 1) / S::BLOCK;
+                scan += item_cost(cache_len(cv, b));
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int x = __shfl_up_sync(0xffffffffu, scan, o);
@@ -698,23 +705,26 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
         int len = cache_len(cv, b);
 
         while (u < u_end) {
-            int blocks = (len + S::BLOCK - 1) / S::BLOCK;
-            while (u >= first + blocks * per_seq) {
-                first += blocks * per_seq;
+            int cost = item_cost(len);
+            while (u >= first + cost * per_seq) {
+                first += cost * per_seq;
                 len = cache_len(cv, ++b);
-                blocks = (len + S::BLOCK - 1) / S::BLOCK;
+                cost = item_cost(len);
             }
-            const int item = (u - first) / blocks;
-            const int item_u0 = first + item * blocks, item_u1 = item_u0 + blocks;
+            const int item = (u - first) / cost;
+            const int item_u0 = first + item * cost, item_u1 = item_u0 + cost;
+            const int blocks = cost - kDecItemCost;
+            // the item's blocks of tokens that are this share's
+            const int lo = max(u - item_u0 - kDecItemCost, 0);
+            const int hi = min(u_end, item_u1) - item_u0 - kDecItemCost;
+            u = min(u_end, item_u1);
+            if (hi <= lo) continue;
             const int kvh = item / p.n_hg, hg = item - kvh * p.n_hg;
-            const int seg_end = min(u_end, item_u1);
-            const int n = seg_end - u;                           // tiles of this warp
-            const int t0 = (u - item_u0) * S::BLOCK + warp * S::TT;  // first token of tile 0
             const int head0 = kvh * p.G + hg * S::HEADS;
             const int n_heads = min(S::HEADS, p.G - hg * S::HEADS);
-            segment(b, len, kvh, head0, n_heads, t0, n);
-            const bool whole = u == item_u0 && seg_end == item_u1;
-            const int part = 2 * cta + (u == item_u0 ? 1 : 0);
+            segment(b, len, kvh, head0, n_heads, lo * S::BLOCK + warp * S::TT, hi - lo);
+            const bool whole = lo == 0 && hi == blocks;
+            const int part = 2 * cta + (lo == 0 ? 1 : 0);
             for (int x = tid; x < S::HEADS * D / 4; x += kDecThreads) {
                 const int h = x / (D / 4), d = x % (D / 4) * 4;
                 float m, lm, l;
@@ -722,19 +732,18 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
                 block_state(h, d, m, lm, l, o);
                 if (!whole) {
                     if (d == 0) {
-                        float *st = p.part_stat + part * 3 * S::HEADS + h;
-                        st[0] = m, st[S::HEADS] = lm, st[2 * S::HEADS] = l;
+                        float *st = p.part_stat + (h * 6 + (lo == 0 ? 1 : 0)) * kDecMaxCtas + cta;
+                        st[0] = m, st[2 * kDecMaxCtas] = lm, st[4 * kDecMaxCtas] = l;
                     }
                     reinterpret_cast<float4 *>(p.part_o + (part * S::HEADS + h) * D + d)[0] = o;
                 } else if (h < n_heads) {
                     store_result<D>(p, b, head0 + h, d, m, lm, l, o);
                 }
             }
-            if (u == item_u0 && tid == 0 && (p.cuts_by_item || !whole))
+            if (lo == 0 && tid == 0 && (p.cuts_by_item || !whole))
                 p.cuts[p.cuts_by_item ? b * per_seq + item : cta] =
                     make_int4(cta, whole ? 0 : cta_of(item_u1 - 1) - cta + 1, b, item);
             __syncthreads();  // the ring is free again
-            u = seg_end;
         }
     } else {
         const uint32_t item = blockIdx.x / p.cluster, rank = blockIdx.x - item * p.cluster;
@@ -807,22 +816,29 @@ __global__ void __launch_bounds__(kDecThreads)
 // The parts of the cut items, weighted by 2^(m_i - max m) and summed in the order
 // of the line, so that the same call gives the same bytes.  Part 0 is the second
 // one of the item's first block, the others the first ones of the blocks behind.
-// It is bound by latency -- a dependent launch, two reads of L2 --, so everything
-// that a thread needs is asked for at once: LANES threads hold a row of O, and
-// work out its statistics among themselves, without shared memory.
-// SPLIT: a block is one query head of an item, its threads split the parts (few
-// items, many parts each: 128K tokens on 4 KV heads are 74 parts an item).
-// Otherwise a block is an item (many items of two or three parts).
+// It is bound by latency -- a dependent launch and two reads of L2, the second of
+// all that the block needs at once: rows and statistics, which each warp works out
+// for itself.
+// SPLIT: a block is 32 elements of one query head of an item, and its threads
+// split the parts: few items, many parts each (128K tokens on 4 KV heads are 74
+// parts an item, joined 3 us after the last of them; 256K tokens on one, 296).
+// Otherwise a block is an item, one of many with a few parts.
 template <int D, int NT, bool SPLIT>
-__global__ void __launch_bounds__(kDecThreads) join_kernel(const __grid_constant__ DecodeParams p) {
-    constexpr int HEADS = 8 * NT, LANES = D / 4, GROUPS = kDecThreads / LANES;
-    constexpr int PER = SPLIT ? GROUPS : 1;  // threads that share a column's parts
-    constexpr int AHEAD = SPLIT ? 8 : 4;
-    __shared__ float4 s_o[kDecThreads];
-    const int tid = threadIdx.x, l4 = tid % LANES, group = tid / LANES;
+__global__ void __launch_bounds__(SPLIT ? kJoinThreads : kDecThreads) join_kernel(const __grid_constant__ DecodeParams p) {
+    constexpr int HEADS = 8 * NT, PIECES = SPLIT ? D / 32 : 1;
+    constexpr int COLS = D / 4 / PIECES;                         // float4s of a row that a block takes
+    constexpr int GROUPS = (SPLIT ? kJoinThreads : kDecThreads) / COLS;
+    constexpr int PER = SPLIT ? GROUPS : 1;                      // threads that share a column's parts
+    constexpr int AHEAD = SPLIT ? kDecMaxCtas / GROUPS : 8;      // parts of a thread under way
+    constexpr int MATES = SPLIT ? 32 : COLS;                     // lanes that work out an item's statistics
+    constexpr int OWN = SPLIT ? (kDecMaxCtas + kJoinThreads - 1) / kJoinThreads : 1;
+    __shared__ float4 s_o[SPLIT ? kJoinThreads : 1];
+    __shared__ float s_st[3][SPLIT ? kDecMaxCtas : 1];           // SPLIT: m, lm, l of the parts
+    const int tid = threadIdx.x, col = tid % COLS, group = tid / COLS;
+    const int l4 = col + (SPLIT ? blockIdx.x % PIECES * COLS : 0);
     launch_dependents();
     wait_for_primary();
-    const int4 cut = __ldcg(p.cuts + (SPLIT ? blockIdx.x / HEADS : blockIdx.x));
+    const int4 cut = __ldcg(p.cuts + (SPLIT ? blockIdx.x / (PIECES * HEADS) : blockIdx.x));
     const int c0 = cut.x, parts = cut.y;
     if (parts == 0) return;
     const int kvh = cut.w / p.n_hg, hg = cut.w - kvh * p.n_hg;
@@ -830,7 +846,20 @@ __global__ void __launch_bounds__(kDecThreads) join_kernel(const __grid_constant
     const int first = SPLIT ? group : 0;
     auto slot_of = [&](int i) { return 2 * (c0 + i) + (i == 0 ? 1 : 0); };
 
-    for (int h = SPLIT ? blockIdx.x % HEADS : group; h < n_heads; h += SPLIT ? HEADS : GROUPS) {
+    for (int h = SPLIT ? blockIdx.x / PIECES % HEADS : group; h < n_heads; h += SPLIT ? HEADS : GROUPS) {
+        // the parts' statistics lie side by side, but part 0's
+        const float *stat = p.part_stat + h * 6 * kDecMaxCtas + c0;
+        auto stat_at = [&](int i, int which) {
+            return __ldcg(stat + (2 * which + (i == 0 ? 1 : 0)) * kDecMaxCtas + i);
+        };
+        float own[OWN][3];
+        if (SPLIT) {
+#pragma unroll
+            for (int k = 0; k < OWN; ++k)
+#pragma unroll
+                for (int which = 0; which < 3; ++which)
+                    own[k][which] = tid + k * kJoinThreads < parts ? stat_at(tid + k * kJoinThreads, which) : 0.f;
+        }
         float4 y[AHEAD];
         float w[AHEAD];
         auto load = [&](int at) {
@@ -840,43 +869,53 @@ __global__ void __launch_bounds__(kDecThreads) join_kernel(const __grid_constant
                 y[k] = make_float4(0.f, 0.f, 0.f, 0.f), w[k] = kDecNone;
                 if (i < parts) {
                     y[k] = __ldcg(reinterpret_cast<const float4 *>(p.part_o + (slot_of(i) * HEADS + h) * D) + l4);
-                    w[k] = __ldcg(p.part_stat + slot_of(i) * 3 * HEADS + h);
+                    if (!SPLIT) w[k] = stat_at(i, 0);
                 }
             }
         };
         load(first);
+        if (SPLIT) {
+#pragma unroll
+            for (int k = 0; k < OWN; ++k)
+                if (tid + k * kJoinThreads < parts)
+#pragma unroll
+                    for (int which = 0; which < 3; ++which) s_st[which][tid + k * kJoinThreads] = own[k][which];
+            __syncthreads();
+        }
         // the item's statistics: a lane's parts in turn, then the lanes'
         float m = kDecNone, lm = kDecNone, l = 0.f;
-#pragma unroll 4
-        for (int i = l4; i < parts; i += LANES) {
-            const float *st = p.part_stat + slot_of(i) * 3 * HEADS + h;
-            const float mi = __ldcg(st), lmi = __ldcg(st + HEADS), li = __ldcg(st + 2 * HEADS);
+        auto add = [&](float lmi, float li) {
             const float top = fmaxf(lm, lmi);
             l = l * exp2_approx(lm - top) + li * exp2_approx(lmi - top);
             lm = top;
-            m = fmaxf(m, mi);
+        };
+#pragma unroll 2
+        for (int i = tid % MATES; i < parts; i += MATES) {
+            m = fmaxf(m, SPLIT ? s_st[0][i] : stat_at(i, 0));
+            add(SPLIT ? s_st[1][i] : stat_at(i, 1), SPLIT ? s_st[2][i] : stat_at(i, 2));
         }
-        const unsigned mates = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << (tid % 32 / LANES * LANES);
+        const unsigned mates = MATES == 32 ? 0xffffffffu : ((1u << MATES) - 1) << (tid % 32 / MATES * MATES);
 #pragma unroll
-        for (int o = 1; o < LANES; o <<= 1) {
+        for (int o = 1; o < MATES; o <<= 1) {
             const float lmi = __shfl_xor_sync(mates, lm, o), li = __shfl_xor_sync(mates, l, o);
-            const float top = fmaxf(lm, lmi);
-            l = l * exp2_approx(lm - top) + li * exp2_approx(lmi - top);
-            lm = top;
+            add(lmi, li);
             m = fmaxf(m, __shfl_xor_sync(mates, m, o));
         }
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int at = first; at < parts; at += AHEAD * PER) {
             if (at != first) load(at);
 #pragma unroll
-            for (int k = 0; k < AHEAD; ++k) add_part(o, y[k], exp2_approx(w[k] - m));
+            for (int k = 0; k < AHEAD; ++k) {
+                if (SPLIT && at + k * PER < parts) w[k] = s_st[0][at + k * PER];
+                add_part(o, y[k], exp2_approx(w[k] - m));
+            }
         }
         if (SPLIT) {
             s_o[tid] = o;
             __syncthreads();
             if (group != 0) return;
-#pragma unroll
-            for (int k = 1; k < PER; ++k) add_part(o, s_o[k * LANES + tid], 1.f);
+#pragma unroll 8
+            for (int k = 1; k < PER; ++k) add_part(o, s_o[k * COLS + tid], 1.f);
         }
         store_result<D>(p, cut.z, head0 + h, l4 * 4, m, lm, l, o);
     }
