@@ -180,7 +180,7 @@ class PagedCache:
     def append(self, rope: QKNormRope, q, k, v, positions, table, lens, q_out=None, workspace=None):
         """``rope.apply(q, k, positions)`` and ``write`` of its keys and of v, in one
         launch; returns the queries.  ``positions`` are the rotation's, [axes, sequences * new]."""
-        return self._calls.append(rope._calls, q, k, v, positions, table, lens, q_out, workspace)
+        return self._calls.append(getattr(rope, "_calls", None), q, k, v, positions, table, lens, q_out, workspace)
 
     def read(self, table, lens, rows, first=0, k_out=None, v_out=None, workspace=None):
         """Positions [first, first + rows) of every sequence as bf16 [sequences, rows,

@@ -112,6 +112,7 @@ def test_cache_type_refused():
 
 @pytest.mark.parametrize("b,expect", [
     (batch(n=-1), 1), (batch(n=1 << 20), 2), (batch(pages=0), 1), (batch(pages=(1 << 31) // 16 + 1), 2),
+    (batch(pages=((1 << 31) - (1 << 16)) // 16 + 1), 2),
     (batch(table=None), 1), (batch(lens=None), 1), (batch(table=FAKE + 2), 3), (batch(lens=FAKE + 1), 3),
 ])
 def test_cache_batch_refused(b, expect):
@@ -120,7 +121,7 @@ def test_cache_batch_refused(b, expect):
 
 @pytest.mark.parametrize("p,kw,expect", [
     (pools(k=None), {}, 1), (pools(v=FAKE + 8), {}, 3), (pools(), dict(dtype=E4M3), 1),
-    (pools(ke=FAKE), dict(dtype=E4M3), 1),
+    (pools(ke=FAKE), dict(dtype=E4M3), 1), (pools(ke=FAKE, ve=FAKE + 8), dict(dtype=E4M3), 3),
 ])
 def test_cache_pools_refused(p, kw, expect):
     assert status_of_all(cache(**kw).c(), p, batch()) == expect
@@ -151,6 +152,9 @@ def test_call_arguments_refused():
     assert lib.spava_cache_read(*h, 0, 1 << 29, FAKE, FAKE, *w) == 2
     assert lib.spava_cache_read(*h, 0, 1, None, FAKE, *w) == 1
     assert lib.spava_cache_read(*h, 0, 1, FAKE, FAKE + 4, *w) == 3
+    # more work units than 32 bits count
+    wide = refs(cache(Hq=32, Hkv=32).c(), pools(), batch(n=1 << 10, pages=1 << 26))
+    assert lib.spava_cache_attn(*wide, FAKE, FAKE, None, *w) == 2
     assert lib.spava_cache_attn(*h, None, FAKE, None, *w) == 1
     assert lib.spava_cache_attn(*h, FAKE, FAKE + 8, None, *w) == 3
     assert lib.spava_cache_attn(*h, FAKE, FAKE, FAKE + 2, *w) == 3

@@ -487,6 +487,123 @@ def test_attn_in_a_graph_follows_lengths_and_tables():
         cu.check_attn(outs[0][0], outs[0][1], q, pools, table, lens, page)
 
 
+def test_a_captured_step_among_copies_and_forks():
+    """A graph of a whole decode step -- copies, a length counted up, append on
+    one stream, attention on another -- replayed token by token, gives what the
+    calls give one by one."""
+    Hq, Hkv, d, page, n = 8, 2, 64, 16, 3
+    g = gen(31)
+    for cap in (64, 1 << 16):                     # short and long tables
+        lay = CacheLayout(Hq, Hkv, d, page_size=page, n_pages=n * 4)
+        table = cu.make_table(n, 4, n * 4, g)
+        wide = widen(table, page, cap) if cap > 64 else table
+        op = QKNormRope(RopeLayout(Hq, Hkv, d), freqs(d), randn(d, g=g), randn(d, g=g))
+        steps = [randn(n, (Hq + 2 * Hkv) * d, g=g) for _ in range(20)]
+        results = []
+        for captured in (False, True):
+            cache = PagedCache(lay)
+            lens = torch.zeros(n, dtype=torch.int32, device="cuda")
+            pos = torch.zeros((1, n), dtype=torch.int32, device="cuda")
+            x = torch.zeros_like(steps[0])
+            src = torch.zeros_like(x)
+            o, lse = torch.empty((n, Hq, d), dtype=BF16, device="cuda"), torch.empty((Hq, n), device="cuda")
+            qa = torch.empty_like(o)
+            other = torch.cuda.Stream()
+
+            def step():
+                x.copy_(src)
+                pos.copy_(lens[None])
+                lens.add_(1)
+                q, k, v = (y.unflatten(1, (-1, d)) for y in x.split([Hq * d, Hkv * d, Hkv * d], 1))
+                cache.append(op, q, k, v, pos, wide, lens, q_out=qa)
+                if captured:
+                    other.wait_stream(torch.cuda.current_stream())
+                    with torch.cuda.stream(other):
+                        cache.attn(qa, wide, lens, o=o, lse=lse)
+                    torch.cuda.current_stream().wait_stream(other)
+                else:
+                    torch.cuda.synchronize()
+                    cache.attn(qa, wide, lens, o=o, lse=lse)
+                    torch.cuda.synchronize()
+
+            if captured:
+                side, gr = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+                side.wait_stream(torch.cuda.current_stream())
+                with torch.cuda.graph(gr, stream=side):
+                    step()
+            out = []
+            for s in steps:
+                src.copy_(s)
+                gr.replay() if captured else step()
+                out.append((o.clone(), lse.clone()))
+            results.append(out + [(cache.k_pages, cache.v_pages)])
+            assert cache.device_status() == 0
+        for a, b in zip(*results):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_a_chain_of_calls_without_waiting():
+    """Hundreds of dependent launches back to back: every call sees what the one
+    before wrote (a cache that is rewritten, read and attended in turn)."""
+    Hq, Hkv, d, page, rows = 28, 4, 128, 16, 300
+    g = gen(32)
+    table = cu.make_table(1, 20, 20, g)
+    lens = torch.tensor([rows], dtype=torch.int32, device="cuda")
+    data = [(randn(rows, Hkv, d, g=g), randn(rows, Hkv, d, g=g), randn(1, Hq, d, g=g)) for _ in range(4)]
+    cache = PagedCache(CacheLayout(Hq, Hkv, d, page_size=page, n_pages=20))
+    want = []
+    for k, v, q in data:
+        cache.write(k, v, table, lens)
+        torch.cuda.synchronize()
+        want.append(cache.attn(q, table, lens))
+        torch.cuda.synchronize()
+    for wide in (False, True):
+        tb = widen(table, page) if wide else table
+        got = []
+        for i in range(200):
+            k, v, q = data[i % 4]
+            cache.write(k, v, tb, lens)
+            got.append((*cache.read(tb, lens, rows), cache.attn(q, tb, lens)[0]))
+        first = got[:4]
+        for i, (k, v, o) in enumerate(got):
+            assert torch.equal(k[0], data[i % 4][0]) and torch.equal(v[0], data[i % 4][1])
+            assert torch.equal(o, first[i % 4][2])
+            if not wide:
+                assert torch.equal(o, want[i % 4][0])
+
+
+def test_threads_share_a_cache():
+    """Calls from several host threads, each on its own stream with its own workspace."""
+    import threading
+    Hq, Hkv, d, page = 28, 4, 128, 16
+    cache, pools, q, table, lt = attn_case([700, 1, 90, 2000], Hq, Hkv, d, page, True, seed=33, extra=0)
+    want = {m: cache.attn(q[:m].contiguous(), table[:m], lt[:m]) for m in (1, 2, 3, 4)}
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(m):
+        try:
+            ws, s = cache.new_workspace(), torch.cuda.Stream()
+            s.wait_stream(torch.cuda.default_stream())
+            with torch.cuda.stream(s):
+                qm, tm, lm = q[:m].contiguous(), table[:m], lt[:m]
+                got = [cache.attn(qm, tm, lm, workspace=ws) for _ in range(100)]
+            s.synchronize()
+            for o, lse in got:
+                if not (torch.equal(o, want[m][0]) and torch.equal(lse, want[m][1])):
+                    bad.append(m)
+        except Exception as e:  # noqa: BLE001
+            bad.append(e)
+
+    torch.cuda.synchronize()
+    threads = [threading.Thread(target=work, args=(m,)) for m in (1, 2, 3, 4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad
+
+
 def test_two_streams_with_their_own_workspaces():
     Hq, Hkv, d, page = 32, 8, 128, 64
     cache, pools, q, table, lt = attn_case([20000, 3000], Hq, Hkv, d, page, True, seed=13, extra=0)
@@ -507,7 +624,9 @@ def test_two_streams_with_their_own_workspaces():
 def test_cache_refusals():
     cache, pools, q, table, lt = attn_case([50, 60], 4, 2, 64, 16, False, seed=14)
     k = randn(2, 2, 64, g=gen(0))
-    for bad in (lambda: cache.attn(q.float(), table, lt), lambda: cache.attn(q[:1], table, lt),
+    for bad in (lambda: cache.attn(None, table, lt), lambda: cache.attn(q, [[0]], lt),
+                lambda: cache.append(None, q, k, k, None, table, lt), lambda: cache.read(table, lt, -1),
+                lambda: cache.attn(q.float(), table, lt), lambda: cache.attn(q[:1], table, lt),
                 lambda: cache.attn(q, table.long(), lt), lambda: cache.attn(q, table[:1], lt),
                 lambda: cache.attn(q, table, lt.cpu()), lambda: cache.attn(q, table.t().contiguous().t(), lt),
                 lambda: cache.attn(q, table, lt, o=torch.empty_like(q[:1])),
