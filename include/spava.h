@@ -419,7 +419,7 @@ typedef struct {
  * replayed with other contents): table int32 [n_seqs, max_pages] and lens int32
  * [n_seqs], the tokens of each sequence, new ones included.  max_pages >= 1,
  * max_pages * page_size <= 2^31 - 2^16, n_seqs < 2^20.  Table entries behind the last
- * page of a sequence are not read.  Sequences may share pages.  A length below
+ * page of a sequence may hold anything.  Sequences may share pages.  A length below
  * 0 counts as 0, one beyond the table as the table's end; a page outside the
  * pool is neither read nor written, its positions count as absent; each of the
  * three sets bit 1 of the workspace status word. */

@@ -60,7 +60,7 @@ def build_calls() -> None:
     compile_to(CALLS, [
         "g++", "-O2", "-std=c++17", "-fPIC", "-shared", *("-I" + d for d in include),
         f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", CALLS_SOURCE, LIB,
-        "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+        "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch", "-ltorch_cpu", "-ltorch_cuda", "-lc10", "-lc10_cuda",
         "-Wl,-rpath,$ORIGIN"])
 
 

@@ -53,14 +53,14 @@ struct CacheView {
 
 // The tokens of sequence b, made to fit the table; out-of-range lengths are
 // reported in the status word.
-__device__ __forceinline__ int cache_len(const CacheView &c, int b) {
-    const int n = c.lens[b];
+__device__ __forceinline__ int fit_len(const CacheView &c, int n) {
     if (n < 0 || n > c.cap) {
         atomicOr(c.status, kStatusBadBatch);
         return n < 0 ? 0 : c.cap;
     }
     return n;
 }
+__device__ __forceinline__ int cache_len(const CacheView &c, int b) { return fit_len(c, c.lens[b]); }
 
 // Pool row of (sequence b, position, KV head 0), kNoRow if its page is outside
 // the pool.  Head h lies h * page_size rows further.

@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Exceptions.h>
@@ -71,7 +72,8 @@ at::Tensor output(PyObject *given, at::IntArrayRef shape, at::ScalarType type, i
         check(t, shape, type, index, name);
         return t;
     }
-    return at::empty(shape, at::TensorOptions().dtype(type).device(at::Device(at::kCUDA, index)));
+    // the caching allocator's memory without a trip through the dispatcher (0.25 us each)
+    return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(index)), std::nullopt);
 }
 
 void *ptr(const at::Tensor &t) { return t.data_ptr(); }

@@ -227,12 +227,94 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
                           warp * (S::PAGES + S::EXPS) + lane * 4;
 
     // ---- the softmax over some of an item's tokens: the tiles t0 + i * STEP, i < n,
-    // of every warp; leaves the warps' states in shared memory
+    // of every warp; leaves the warps' states in shared memory.  A cluster's block
+    // gives its sequence's length as it is in memory, and n as what its share is
+    // rounded up by.
     const int STEP = CLUSTER ? p.cluster * S::BLOCK : S::BLOCK;
     float *sm_o = reinterpret_cast<float *>(smem);          // [warps][HEADS][OPAD]
     float *sm_st = sm_o + kDecWarps * S::HEADS * S::OPAD;   // [3][warps][HEADS]: m, lm, l
     auto segment = [&](int b, int len, int kvh, int head0, int n_heads, int t0, int n) {
         const uint32_t head_rows = static_cast<uint32_t>(kvh) * cv.page.d;
+
+        // ---- the ring
+        // Lane i takes care of the tokens i, i + 32 of a tile (i % 16 where a tile
+        // has 16): their table entries come by cp.async too, K tiles before the
+        // rows that they lead to are asked for, as a load that a register waits
+        // for would hold up the warp (measured: 58 instead of 43 us for a stream
+        // of 268 MB).
+        constexpr int RW = S::RW, K = kDecStages - 1;
+        const int32_t *table = cv.table + b * cv.max_pages;
+        auto token = [&](int i, int k) {
+            return static_cast<int64_t>(t0) + static_cast<int64_t>(i) * STEP +
+                   (S::TT == 16 ? lane % 16 : lane + 32 * k);
+        };
+        auto held_token = [&](int i, int64_t t) { return i < n && t < len; };
+        auto row_of = [&](int i, int k, int page) {  // pool row of this lane's k-th token of tile i
+            const int64_t t = token(i, k);
+            if (!held_token(i, t)) return kNoRow;
+            if (static_cast<uint32_t>(page) >= cv.n_pages) {
+                atomicOr(cv.status, kStatusBadBatch);
+                return kNoRow;
+            }
+            uint32_t off;
+            cv.page.quot(static_cast<uint32_t>(t), off);
+            return static_cast<uint32_t>(page) * cv.Hkv * cv.page.d + head_rows + off;
+        };
+        auto issue = [&](int stage, const uint32_t (&r)[RW]) {
+            if (E4M3) {
+                // the aligned word with the row's exponent; its end may lie behind the pool's
+#pragma unroll
+                for (int k = 0; k < RW; ++k) {
+                    const uint32_t at = r[k] & ~3u, to = side + S::PAGES + (stage * RW + k) * 256;
+                    const uint32_t bytes = r[k] == kNoRow ? 0 : min(4u, cv.n_rows - at);
+                    cp_async4(to, cv.k_exp + (bytes ? at : 0), bytes);
+                    cp_async4(to + 128, cv.v_exp + (bytes ? at : 0), bytes);
+                }
+            }
+            const uint32_t dst = ring + stage * kDecTileBytes;
+            const int piece = lane % S::LPR;
+#pragma unroll
+            for (int x = 0; x < 8; ++x) {
+                const int at = x * S::RPI + lane / S::LPR;  // row of the tile
+                const uint32_t row = __shfl_sync(0xffffffffu, r[x * S::RPI / 32], at % 32);
+                const int64_t from = row == kNoRow ? 0 : static_cast<int64_t>(row) * S::ROW + piece * 16;
+                const uint32_t bytes = row == kNoRow ? 0 : 16;
+                cp_async16(dst + at * S::ROW + (piece ^ S::k_swizzle(at)) * 16,
+                           static_cast<const char *>(cv.k) + from, bytes);
+                cp_async16(dst + kDecTileBytes / 2 + at * S::ROW + (piece ^ S::v_swizzle(at)) * 16,
+                           static_cast<const char *>(cv.v) + from, bytes);
+            }
+        };
+        uint32_t rows[kDecStages][RW];  // of the tiles i, i + 1, ... in flight
+        {
+            // of the tiles 0 ... 2 K; a cluster's block, whose length is still on its
+            // way, asks for them as if its table were full
+            int page[2 * K + 1][RW];
+#pragma unroll
+            for (int i = 0; i <= 2 * K; ++i)
+#pragma unroll
+                for (int k = 0; k < RW; ++k) {
+                    const int64_t t = token(i, k);
+                    page[i][k] = (CLUSTER ? t < cv.cap : held_token(i, t))
+                                     ? table[cv.page.quot(static_cast<uint32_t>(t))]
+                                     : 0;
+                }
+            if (CLUSTER) {
+                len = fit_len(cv, len);
+                n = ((len + S::BLOCK - 1) / S::BLOCK + n) / p.cluster;
+            }
+#pragma unroll
+            for (int i = 0; i < K; ++i) {
+#pragma unroll
+                for (int k = 0; k < RW; ++k) rows[i][k] = row_of(i, k, page[i][k]);
+                issue(i, rows[i]);
+                cp_async_commit();
+            }
+#pragma unroll
+            for (int i = K; i <= 2 * K; ++i)
+#pragma unroll
+                for (int k = 0; k < RW; ++k) sts4(side + ((i % kDecPageSlots) * RW + k) * 128, page[i][k]);
+        }
 
         // ---- q: the MMA's B operand, and its scale
         uint32_t qf[NT][S::KS][2];
@@ -290,78 +372,6 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
                 for (int k = 0; k < 4; ++k) acc[t][i][k] = 0.f;
 #pragma unroll
             for (int k = 0; k < 2; ++k) m_ref[t][k] = l_ref[t][k] = kDecNone, l_sum[t][k] = 0.f;
-        }
-
-        // ---- the ring
-        // Lane i takes care of the tokens i, i + 32 of a tile (i % 16 where a tile
-        // has 16): their table entries come by cp.async too, K tiles before the
-        // rows that they lead to are asked for, as a load that a register waits
-        // for would hold up the warp (measured: 58 instead of 43 us for a stream
-        // of 268 MB).
-        constexpr int RW = S::RW, K = kDecStages - 1;
-        const int32_t *table = cv.table + b * cv.max_pages;
-        auto token = [&](int i, int k) {
-            return static_cast<int64_t>(t0) + static_cast<int64_t>(i) * STEP +
-                   (S::TT == 16 ? lane % 16 : lane + 32 * k);
-        };
-        auto held_token = [&](int i, int64_t t) { return i < n && t < len; };
-        auto row_of = [&](int i, int k, int page) {  // pool row of this lane's k-th token of tile i
-            const int64_t t = token(i, k);
-            if (!held_token(i, t)) return kNoRow;
-            if (static_cast<uint32_t>(page) >= cv.n_pages) {
-                atomicOr(cv.status, kStatusBadBatch);
-                return kNoRow;
-            }
-            uint32_t off;
-            cv.page.quot(static_cast<uint32_t>(t), off);
-            return static_cast<uint32_t>(page) * cv.Hkv * cv.page.d + head_rows + off;
-        };
-        auto issue = [&](int stage, const uint32_t (&r)[RW]) {
-            if (E4M3) {
-                // the aligned word with the row's exponent; its end may lie behind the pool's
-#pragma unroll
-                for (int k = 0; k < RW; ++k) {
-                    const uint32_t at = r[k] & ~3u, to = side + S::PAGES + (stage * RW + k) * 256;
-                    const uint32_t bytes = r[k] == kNoRow ? 0 : min(4u, cv.n_rows - at);
-                    cp_async4(to, cv.k_exp + (bytes ? at : 0), bytes);
-                    cp_async4(to + 128, cv.v_exp + (bytes ? at : 0), bytes);
-                }
-            }
-            const uint32_t dst = ring + stage * kDecTileBytes;
-            const int piece = lane % S::LPR;
-#pragma unroll
-            for (int x = 0; x < 8; ++x) {
-                const int at = x * S::RPI + lane / S::LPR;  // row of the tile
-                const uint32_t row = __shfl_sync(0xffffffffu, r[x * S::RPI / 32], at % 32);
-                const int64_t from = row == kNoRow ? 0 : static_cast<int64_t>(row) * S::ROW + piece * 16;
-                const uint32_t bytes = row == kNoRow ? 0 : 16;
-                cp_async16(dst + at * S::ROW + (piece ^ S::k_swizzle(at)) * 16,
-                           static_cast<const char *>(cv.k) + from, bytes);
-                cp_async16(dst + kDecTileBytes / 2 + at * S::ROW + (piece ^ S::v_swizzle(at)) * 16,
-                           static_cast<const char *>(cv.v) + from, bytes);
-            }
-        };
-        uint32_t rows[kDecStages][RW];  // of the tiles i, i + 1, ... in flight
-        {
-            int page[2 * K + 1][RW];  // of the tiles 0 ... 2 K
-#pragma unroll
-            for (int i = 0; i <= 2 * K; ++i)
-#pragma unroll
-                for (int k = 0; k < RW; ++k) {
-                    const int64_t t = token(i, k);
-                    page[i][k] = held_token(i, t) ? table[cv.page.quot(static_cast<uint32_t>(t))] : 0;
-                }
-#pragma unroll
-            for (int i = 0; i < K; ++i) {
-#pragma unroll
-                for (int k = 0; k < RW; ++k) rows[i][k] = row_of(i, k, page[i][k]);
-                issue(i, rows[i]);
-                cp_async_commit();
-            }
-#pragma unroll
-            for (int i = K; i <= 2 * K; ++i)
-#pragma unroll
-                for (int k = 0; k < RW; ++k) sts4(side + ((i % kDecPageSlots) * RW + k) * 128, page[i][k]);
         }
 
         int stage = 0, slot = K % kDecPageSlots;  // slot: of tile i + K's table entries
@@ -751,10 +761,8 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
         const int kvh = in_seq / p.n_hg, hg = in_seq - kvh * p.n_hg;
         const int head0 = kvh * p.G + hg * S::HEADS;
         const int n_heads = min(S::HEADS, p.G - hg * S::HEADS);
-        const int len = cache_len(cv, b);
-        const int blocks = (len + S::BLOCK - 1) / S::BLOCK;
-        segment(b, len, kvh, head0, n_heads, rank * S::BLOCK + warp * S::TT,
-                (blocks + p.cluster - 1 - static_cast<int>(rank)) / p.cluster);
+        segment(b, cv.lens[b], kvh, head0, n_heads, rank * S::BLOCK + warp * S::TT,
+                p.cluster - 1 - static_cast<int>(rank));
         // the block's state, for the others to read
         float *cl_o = sm_st + 3 * kDecWarps * S::HEADS;  // [HEADS][D]
         float *cl_st = cl_o + S::HEADS * D;              // [3][HEADS]
