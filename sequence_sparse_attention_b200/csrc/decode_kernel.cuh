@@ -635,24 +635,22 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
         auto item_cost = [](int len) { return len > 0 ? (len + S::BLOCK - 1) / S::BLOCK + kDecItemCost : 0; };
         __shared__ int s_prefix[kDecThreads + 1];
         __shared__ int s_warp[kDecWarps];
-        // ---- the line of units: sequence groups of `per`, s_prefix[i] the unit where group i begins
-        int per, total;
-        bool empty;  // there are sequences without positions
-        if (cv.n_seqs <= 32) {
-            // every warp for itself, from one load: no barrier
-            per = 1;
-            const int len = lane < cv.n_seqs ? cache_len(cv, lane) : 1;
-            empty = __any_sync(0xffffffffu, len == 0);
-            int scan = lane < cv.n_seqs ? item_cost(len) * per_seq : 0;
+        // ---- the line of units.  Up to 32 sequences: every warp for itself, a lane a
+        // sequence, without a barrier.  More: groups of `per`, s_prefix[i] the unit
+        // where group i begins.
+        const bool few = cv.n_seqs <= 32;
+        int per = 1, total, lane_len = 1, lane_end = 0;  // lane_end: the unit behind the lane's sequence
+        bool empty = true;                               // there may be sequences without positions
+        if (few) {
+            if (lane < cv.n_seqs) lane_len = cache_len(cv, lane);
+            empty = __any_sync(0xffffffffu, lane_len == 0);
+            lane_end = lane < cv.n_seqs ? item_cost(lane_len) * per_seq : 0;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
-                const int x = __shfl_up_sync(0xffffffffu, scan, o);
-                if (lane >= o) scan += x;
+                const int x = __shfl_up_sync(0xffffffffu, lane_end, o);
+                if (lane >= o) lane_end += x;
             }
-            s_prefix[lane + 1] = scan;  // the same values from every warp
-            if (lane == 0) s_prefix[0] = 0;
-            __syncwarp();
-            total = __shfl_sync(0xffffffffu, scan, 31);
+            total = __shfl_sync(0xffffffffu, lane_end, 31);
         } else {
             per = (cv.n_seqs + kDecThreads - 1) / kDecThreads;
             int scan = 0;
@@ -672,7 +670,6 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
             if (tid == 0) s_prefix[0] = 0;
             __syncthreads();
             total = s_prefix[kDecThreads];
-            empty = true;
         }
 
         // ---- sequences without positions
@@ -702,17 +699,21 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
         };
 
         // ---- the sequence of the first unit
-        int b, first;  // first: the unit where sequence b begins
-        {
-            int lo = 0, hi = cv.n_seqs <= 32 ? 32 : kDecThreads;  // s_prefix[lo] <= u < s_prefix[hi]
+        int b, first, len;  // first: the unit where sequence b begins
+        if (few) {
+            b = __ffs(__ballot_sync(0xffffffffu, lane_end > u)) - 1;
+            len = __shfl_sync(0xffffffffu, lane_len, b);
+            first = __shfl_sync(0xffffffffu, lane_end, b) - item_cost(len) * per_seq;
+        } else {
+            int lo = 0, hi = kDecThreads;  // s_prefix[lo] <= u < s_prefix[hi]
             while (hi - lo > 1) {
                 const int mid = (lo + hi) / 2;
                 if (s_prefix[mid] <= u) lo = mid; else hi = mid;
             }
             b = lo * per;
             first = s_prefix[lo];
+            len = cache_len(cv, b);
         }
-        int len = cache_len(cv, b);
 
         while (u < u_end) {
             int cost = item_cost(len);
