@@ -64,6 +64,9 @@ spava_status check_rows(const void *p, int64_t stride, int heads, int d) {
 
 constexpr size_t kCutBytes = sizeof(int4) * kDecMaxCtas;
 
+// Query heads of a KV head in tiles of 8, or two tiles at a time: more than 8 in
+// two goes would read the rows twice (262144 tokens, 16 heads on one: 31.5 us, 39.7
+// in two goes), while two tiles cost registers that fewer heads do not need.
 int head_tile(const spava_cache_config *c) { return c->n_q_heads / c->n_kv_heads > 8 ? 2 : 1; }
 
 // [status block 256 | cut items | partial statistics | partial O]
@@ -109,12 +112,17 @@ spava_status make_view(const spava_cache_config *c, const spava_cache_pools *p,
 }
 
 // Tokens of a block (a power of two up to `most`) and blocks that share their
-// items: few tokens are spread over the SMs head by head, many share what a
-// block makes for them.  per_pass: items a block works on at a time.
+// items, per_pass of which a block works on at a time: enough tokens to fill a
+// pass, then more where there are plenty, as a block's tokens share what it makes
+// for them; few tokens are spread over the SMs head by head.  (Norm, rotation and
+// write of 64 tokens, 48 heads: 3.1 us, 10.5 with eight tokens a block and no
+// sharing out.  Norm of 131072 tokens: 356 us, 370 with four tokens a block.)
 void split_tokens(int64_t n_rows, int64_t heads, int most, int per_pass, int32_t *tokens_log2, int64_t *splits) {
     constexpr int kBlocks = 148 * 4;  // enough to fill the SMs
     int lg = 0;
-    while ((2 << lg) <= most && (n_rows >> (lg + 1)) >= kBlocks) ++lg;
+    while ((2 << lg) <= most && (((heads << lg) < per_pass && (1LL << lg) < n_rows) ||
+                                 (n_rows >> (lg + 1)) >= kBlocks))
+        ++lg;
     const int64_t groups = (n_rows + (1LL << lg) - 1) >> lg, passes = ((heads << lg) + per_pass - 1) / per_pass;
     *tokens_log2 = lg;
     *splits = std::max<int64_t>(1, std::min(passes, kBlocks / groups));
@@ -177,10 +185,15 @@ spava_status set_dynamic_smem(K kernel, int bytes, std::atomic<uint64_t> &done, 
     return SPAVA_OK;
 }
 
-// decode_cluster_kernel takes batches whose items (sequence, KV head, query head
-// group) fit the SMs at once, and whose tables hold at most so many bytes of K and
-// V rows for each block of an item's cluster.
-constexpr int64_t kClusterBlockBytes = 256 << 10;
+// Whether decode_cluster_kernel takes a batch, of `blocks` blocks with tables of at
+// most `kib` KiB of K and V rows each.  A block streams 50 KiB a us, all of them
+// 6500, and the line's second launch and join cost 2.3 us more: clusters win where
+// kib / 50 < 2.3 + blocks * kib / 6500 -- if the sequences are as long as their
+// tables; the lengths are not known here, and 256 KiB bound what that can cost.
+// By the line / by clusters, device time in us, bf16, 4 KV heads: one sequence (32
+// blocks) of 512 tokens 6.8 / 4.9, 2048 (128 KiB) 7.3 / 6.7, 4096 7.4 / 9.4; 4
+// sequences (128 blocks) of 4096 13.4 / 11.7; 16 (256 blocks) of 1024 11.5 / 9.4.
+bool by_clusters(int64_t blocks, int64_t kib) { return kib <= 256 && kib * (130 - blocks) <= 15000; }
 
 template <int D, bool E4M3, int NT>
 spava_status launch_decode(DecodeParams &p, int64_t max_units, cudaStream_t st) {
@@ -192,9 +205,10 @@ spava_status launch_decode(DecodeParams &p, int64_t max_units, cudaStream_t st) 
     const int64_t items = int64_t(p.cache.n_seqs) * p.cache.Hkv * p.n_hg;
     p.cluster = kDecCluster;
     while (p.cluster > 1 && items * p.cluster > 2 * n_sm) p.cluster /= 2;
-    if (items * p.cluster <= 2 * n_sm && int64_t(p.cache.cap) * 2 * S::ROW <= kClusterBlockBytes * p.cluster) {
+    const int64_t blocks = items * p.cluster;
+    if (blocks <= 2 * n_sm && by_clusters(blocks, int64_t(p.cache.cap) * 2 * S::ROW / 1024 / p.cluster)) {
         SPAVA_TRY(set_dynamic_smem(decode_cluster_kernel<D, E4M3, NT>, S::SMEM, cluster_done, dev));
-        return launch(decode_cluster_kernel<D, E4M3, NT>, static_cast<unsigned>(items * p.cluster), kDecThreads,
+        return launch(decode_cluster_kernel<D, E4M3, NT>, static_cast<unsigned>(blocks), kDecThreads,
                       S::SMEM, p.cluster, st, p);
     }
     SPAVA_TRY(set_dynamic_smem(decode_kernel<D, E4M3, NT>, S::SMEM, done, dev));
@@ -203,9 +217,12 @@ spava_status launch_decode(DecodeParams &p, int64_t max_units, cudaStream_t st) 
     p.cuts_by_item = items <= grid;
     SPAVA_TRY(launch(decode_kernel<D, E4M3, NT>, grid, kDecThreads, S::SMEM, 1, st, p));
     const int cuts = static_cast<int>(std::min<int64_t>(items, grid));
-    constexpr int kSplitBlocks = 8 * NT * (D / 32);  // of an item
-    const bool split = cuts * kSplitBlocks <= 2 * grid;
-    return launch(split ? join_kernel<D, NT, true> : join_kernel<D, NT, false>, split ? cuts * kSplitBlocks : cuts,
+    // Items of 16 parts and more are split further (131072 tokens on 4 KV heads,
+    // 74 parts: 48.4 us, 59.5 without; 16 sequences on one, 18 parts: 35.1, 41.0;
+    // 32 items of 9 parts: 51.1, 48.8 without).
+    const bool split = items * 16 <= grid;
+    constexpr int kSplitBlocks = 8 * NT * (D / 32), kBlocks = 8 * NT * D / 4 / kDecThreads;  // of an item
+    return launch(split ? join_kernel<D, NT, true> : join_kernel<D, NT, false>, cuts * (split ? kSplitBlocks : kBlocks),
                   split ? kJoinThreads : kDecThreads, 0, 1, st, p);
 }
 

@@ -261,7 +261,8 @@ ATTN_CASES = [
     ([15, 16, 17, 31, 32, 33], 14, 2, 64, 8), ([63, 64, 65, 127, 128, 129], 28, 4, 128, 24),
     ([255, 256, 257], 9, 1, 64, 48), ([1000, 1, 700], 16, 1, 128, 1), ([511], 40, 2, 128, 100),
     ([5000], 28, 4, 128, 64), ([4097, 0, 2048, 33], 32, 8, 128, 16), ([20011], 24, 2, 64, 256),
-    ([300] * 200, 4, 4, 64, 64), (list(range(0, 400)), 6, 3, 128, 7), ([65536], 17, 1, 128, 64),
+    ([300] * 200, 4, 4, 64, 64), (list(range(0, 400)), 6, 3, 128, 7), ([65536], 17, 1, 128, 64),    # 64, 128 and 204 items: clusters of 4, 2 and 1 blocks where the tables are short
+    ([50, 130, 0, 700] * 4, 28, 4, 128, 16), ([33, 90] * 16, 12, 4, 64, 24), ([20, 400, 61] * 17, 40, 4, 128, 64),
 ]
 
 
