@@ -133,7 +133,9 @@ class PagedCache:
     [sequences, max_pages]) and ``lens`` (int32 [sequences]) stay on the device.
 
     Calls that may run at the same time (other streams, graphs replayed side by
-    side) need workspaces of their own: ``new_workspace()`` and ``workspace=``."""
+    side) need workspaces of their own: ``new_workspace()`` and ``workspace=``.
+    Caches of the same heads whose calls follow each other, as those of a model's
+    layers do, can share one."""
 
     def __init__(self, lay: CacheLayout, device="cuda", k_pages=None, v_pages=None, k_exp=None, v_exp=None,
                  workspace=None):
