@@ -116,12 +116,14 @@ spava_status make_view(const spava_cache_config *c, const spava_cache_pools *p,
 // pass, then more where there are plenty, as a block's tokens share what it makes
 // for them; few tokens are spread over the SMs head by head.  (Norm, rotation and
 // write of 64 tokens, 48 heads: 3.1 us, 10.5 with eight tokens a block and no
-// sharing out.  Norm of 131072 tokens: 356 us, 370 with four tokens a block.)
+// sharing out.  Norm of 131072 tokens: 353 us, 370 with four tokens a block; of 5000:
+// 18.4 us, 20.8 where half as many blocks are plenty.)
 void split_tokens(int64_t n_rows, int64_t heads, int most, int per_pass, int32_t *tokens_log2, int64_t *splits) {
     constexpr int kBlocks = 148 * 4;  // enough to fill the SMs
+    constexpr int kPlenty = 2 * kBlocks;
     int lg = 0;
     while ((2 << lg) <= most && (((heads << lg) < per_pass && (1LL << lg) < n_rows) ||
-                                 (n_rows >> (lg + 1)) >= kBlocks))
+                                 ((n_rows >> (lg + 1)) >= kPlenty && (heads << (lg + 1)) <= 8 * per_pass)))
         ++lg;
     const int64_t groups = (n_rows + (1LL << lg) - 1) >> lg, passes = ((heads << lg) + per_pass - 1) / per_pass;
     *tokens_log2 = lg;
@@ -134,7 +136,7 @@ spava_status launch_rows(RowParams &p, int d, cudaStream_t st) {
     if (p.n_rows == 0) return SPAVA_OK;
     if (p.n_rows >= (1LL << 31) / heads) return SPAVA_ERR_UNSUPPORTED;
     int64_t splits;
-    split_tokens(p.n_rows, heads, kRowTokens, kRowThreads / (d / 16), &p.tokens_log2, &splits);
+    split_tokens(p.n_rows, heads, ROPE ? kRowTokens : kWriteTokens, kRowThreads / (d / 16), &p.tokens_log2, &splits);
     p.splits = FastDiv::of(static_cast<uint32_t>(splits));
     const int64_t groups = (p.n_rows + (1LL << p.tokens_log2) - 1) >> p.tokens_log2;
     return launch(d == 64 ? row_kernel<64, CACHE, ROPE> : row_kernel<128, CACHE, ROPE>,
@@ -195,10 +197,20 @@ spava_status set_dynamic_smem(K kernel, int bytes, std::atomic<uint64_t> &done, 
 // sequences (128 blocks) of 4096 13.4 / 11.7; 16 (256 blocks) of 1024 11.5 / 9.4.
 bool by_clusters(int64_t blocks, int64_t kib) { return kib <= 256 && kib * (130 - blocks) <= 15000; }
 
+// Whether decode_warp_kernel takes a batch, whose tables hold at most `tiles` tiles
+// (8 KiB of K and V rows): always up to two, up to 8 where there are too many items
+// for clusters, up to 16 where there are many more.  By the line or clusters / by
+// warps, device time in us: one sequence of 32 tokens, 4 KV heads, bf16 4.3 / 3.2
+// (of 64, four tiles, 4.4 / 4.4); 100 sequences of 64, 8 KV heads, e4m3 13.2 / 5.6;
+// 40 of 500 (320 items, 16 tiles) 16.6 / 22.7, 100 (800 items) 28.5 / 24.0.
+bool by_warps(int64_t tiles, int64_t items, int64_t slots) {
+    return tiles <= (items <= slots ? 2 : items < 2 * slots ? 8 : 16);
+}
+
 template <int D, bool E4M3, int NT>
 spava_status launch_decode(DecodeParams &p, int64_t max_units, cudaStream_t st) {
     using S = DecodeShape<D, E4M3, NT>;
-    static std::atomic<uint64_t> done{0}, cluster_done{0};
+    static std::atomic<uint64_t> done{0}, cluster_done{0}, warp_done{0};
     int dev = 0, n_sm = 0;
     SPAVA_CUDA(cudaGetDevice(&dev));
     SPAVA_CUDA(cudaDeviceGetAttribute(&n_sm, cudaDevAttrMultiProcessorCount, dev));
@@ -206,6 +218,11 @@ spava_status launch_decode(DecodeParams &p, int64_t max_units, cudaStream_t st) 
     p.cluster = kDecCluster;
     while (p.cluster > 1 && items * p.cluster > 2 * n_sm) p.cluster /= 2;
     const int64_t blocks = items * p.cluster;
+    if (by_warps((p.cache.cap + S::TT - 1) / S::TT, items, 2 * n_sm) && items < (1LL << 31)) {
+        SPAVA_TRY(set_dynamic_smem(decode_warp_kernel<D, E4M3, NT>, S::SMEM, warp_done, dev));
+        return launch(decode_warp_kernel<D, E4M3, NT>, static_cast<unsigned>((items + kDecWarps - 1) / kDecWarps),
+                      kDecThreads, S::SMEM, 1, st, p);
+    }
     if (blocks <= 2 * n_sm && by_clusters(blocks, int64_t(p.cache.cap) * 2 * S::ROW / 1024 / p.cluster)) {
         SPAVA_TRY(set_dynamic_smem(decode_cluster_kernel<D, E4M3, NT>, S::SMEM, cluster_done, dev));
         return launch(decode_cluster_kernel<D, E4M3, NT>, static_cast<unsigned>(blocks), kDecThreads,

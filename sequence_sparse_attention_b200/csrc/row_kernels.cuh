@@ -4,8 +4,7 @@
 //
 // All three are bound by memory (every row is read once and written once) as
 // long as the work beside it stays small; what tokens share -- angles, weights,
-// cache places -- is made once a block, in shared memory, for up to eight
-// tokens, and rows are taken heads outside, tokens inside.
+// cache places -- is made once a block, in shared memory, and rows are taken heads outside, tokens inside.
 #pragma once
 
 #include "cache_common.cuh"
@@ -14,7 +13,8 @@
 namespace spava {
 
 constexpr int kRowThreads = 256;
-constexpr int kRowTokens = 8;   // most tokens of a row_kernel block
+constexpr int kRowTokens = 16;    // most tokens of a row_kernel block with tables,
+constexpr int kWriteTokens = 32;  // of one without
 constexpr int kReadTokens = 16;  // of a read_kernel block
 
 struct RowParams {
@@ -121,7 +121,7 @@ __device__ __forceinline__ void turn2(float2 &a, float2 &b, float2 cs, float2 sn
 // any 31-bit position, where a 32-bit product is off by up to 2^-24 of the
 // angle itself (0.008 radians at position 131072).
 //
-// Measured, 28/4 heads of 128: 131072 tokens 356 us, 6.0 TB/s read and written (0.92
+// Measured, 28/4 heads of 128: 131072 tokens 353 us, 6.1 TB/s read and written (0.92
 // of the copy rate); 16384 tokens 48.8 us; e4m3 write of 16384 tokens, 4 KV heads,
 // 10.8 us; one token with its write 2.7 us.
 //
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(kRowThreads, ROPE ? 4 : 7) row_kernel(const __
     // What lane l needs is float4 [..][l] of a table: no bank conflicts.
     __shared__ float4 s_w[2][4][L];                          // weights: chunk c0, then c1
     __shared__ float4 s_cs[ROPE ? kRowTokens : 1][4][L];     // cosines (c0's or the pairs' first four), ...
-    __shared__ uint32_t s_slot[kRowTokens];
+    __shared__ uint32_t s_slot[kWriteTokens];
     launch_dependents();
     wait_for_primary();
 
@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kRowThreads, ROPE ? 4 : 7) row_kernel(const __
     Item x = load(at);
 
     // ---- what the block's tokens share
-    if (CACHE && tid >= kRowThreads - kRowTokens) {
-        const int t = tid - (kRowThreads - kRowTokens);
+    if (CACHE && tid >= kRowThreads - kWriteTokens) {
+        const int t = tid - (kRowThreads - kWriteTokens);
         s_slot[t] = t < n_tok ? row_slot(p, row0 + t) : kNoRow;
     }
     if (ROPE) {
