@@ -1,5 +1,7 @@
 // decode_kernel.cuh -- attention of one new token per sequence over the paged
-// cache, split over the cache's length and joined in the same launch.
+// cache: along a line of equal shares (decode_kernel, whose parts join_kernel
+// joins), an item a cluster (decode_cluster_kernel) or an item a warp
+// (decode_warp_kernel), as the batch and its tables' room have it.
 #pragma once
 
 #include "cache_common.cuh"
@@ -9,8 +11,8 @@ namespace spava {
 constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kJoinThreads = 256;  // of a join block that shares its parts out
-constexpr int kDecCluster = 8;    // most blocks of decode_cluster_kernel's clusters
-constexpr int kDecMaxCtas = 320;  // the workspace's partials are sized for these
+constexpr int kDecCluster = 8;     // most blocks of decode_cluster_kernel's clusters
+constexpr int kDecMaxCtas = 320;   // the workspace's partials are sized for these
 // Beginning and ending an item takes a block about as long as two units of its
 // tokens, and counts as that: 17 sequences of 100 to 16100 tokens take 55 us, 70
 // where only tokens count and some block gets the many short items (e4m3, 8 KV heads).
@@ -39,7 +41,7 @@ struct DecodeParams {
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global.L2::256B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src),
                  "r"(bytes)
                  : "memory");
 }
@@ -182,7 +184,6 @@ struct DecodeShape {
     static constexpr int OPAD = D + 4;                     // floats of an O row in shared memory
     // The ring is free when a segment ends, and takes the warps' O and statistics.
     static constexpr int MERGE = kDecWarps * HEADS * (OPAD + 3) * 4;
-    static constexpr int ROWS4 = HEADS * D / 128;          // float4s of a partial O per lane of a warp
     static constexpr int RING = MERGE > kDecRingBytes ? MERGE : kDecRingBytes;
     // behind it: table entries and, of an e4m3 cache, the words with the rows' exponents
     static constexpr int RW = TT == 64 ? 2 : 1;            // tokens of a tile per lane
@@ -254,9 +255,9 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
         // ---- the ring
         // Lane i takes care of the tokens i, i + 32 of a tile (i % 16 where a tile
         // has 16): their table entries come by cp.async too, K tiles before the
-        // rows that they lead to are asked for, as a load that a register waits
-        // for would hold up the warp (measured: 58 instead of 43 us for a stream
-        // of 268 MB).
+        // rows that they lead to are asked for, as a load that a register waits for
+        // would hold up the warp (24 ragged sequences, e4m3: 95 instead of 106 us,
+        // before other steps).
         constexpr int RW = S::RW, K = kDecStages - 1;
         const int32_t *table = cv.table + b * cv.max_pages;
         auto token = [&](int i, int k) {
