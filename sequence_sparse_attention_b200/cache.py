@@ -12,18 +12,13 @@ graph.  Inference only: no gradients.
 from __future__ import annotations
 
 import ctypes
+import functools
 from dataclasses import dataclass
 
 import torch
 
 from . import native
 from .native import SpavaCacheConfig, SpavaCachePools, SpavaRopeConfig
-
-try:
-    from . import _calls
-except ImportError as e:
-    raise ImportError("_calls.so is missing or does not load: build it with "
-                      "`python -m sequence_sparse_attention_b200.build`") from e
 
 _CACHE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
 
@@ -95,7 +90,16 @@ def _failed(name, status):
     raise native.SpavaError(name, status, native.load().spava_last_cuda_error() if status == 5 else 0)
 
 
-_calls.on_failure(_failed)
+@functools.cache
+def _load_calls():
+    """The compiled calls; loaded at first use, as the package that builds them must import without."""
+    try:
+        from . import _calls
+    except ImportError as e:
+        raise ImportError("_calls.so is missing or does not load: build it with "
+                          "`python -m sequence_sparse_attention_b200.build`") from e
+    _calls.on_failure(_failed)
+    return _calls
 
 
 class QKNormRope:
@@ -116,7 +120,7 @@ class QKNormRope:
             if t is not None:
                 _check(t, (lay.d,), torch.bfloat16, index, name)
         self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight
-        self._calls = _calls.Rope(ctypes.addressof(self.cfg), *(0 if t is None else t.data_ptr()
+        self._calls = _load_calls().Rope(ctypes.addressof(self.cfg), *(0 if t is None else t.data_ptr()
                                                                 for t in (q_weight, k_weight, inv_freq)), index)
 
     def apply(self, q, k, positions=None, q_out=None, k_out=None):
@@ -163,7 +167,7 @@ class PagedCache:
         _check(self.workspace, (self.workspace.numel(),), torch.uint8, index, "workspace")
         pools = SpavaCachePools(*(None if t is None else t.data_ptr()
                                   for t in (self.k_pages, self.v_pages, self.k_exp, self.v_exp)))
-        self._calls = _calls.Cache(ctypes.addressof(self.cfg), ctypes.addressof(pools), self.workspace.data_ptr(),
+        self._calls = _load_calls().Cache(ctypes.addressof(self.cfg), ctypes.addressof(pools), self.workspace.data_ptr(),
                                    self.workspace.numel(), index)
 
     @property

@@ -152,6 +152,10 @@ int rope_init(PyObject *self, PyObject *args, PyObject *) {
     Rope *r = reinterpret_cast<Rope *>(self);
     unsigned long long cfg, q, k, f;
     if (!PyArg_ParseTuple(args, "KKKKi", &cfg, &q, &k, &f, &r->index)) return -1;
+    if (!cfg) {
+        PyErr_SetString(PyExc_ValueError, "Rope: no configuration");
+        return -1;
+    }
     r->cfg = *reinterpret_cast<const spava_rope_config *>(cfg);
     r->q_weight = reinterpret_cast<const void *>(q);
     r->k_weight = reinterpret_cast<const void *>(k);
@@ -215,6 +219,10 @@ int cache_init(PyObject *self, PyObject *args, PyObject *) {
     Cache *c = reinterpret_cast<Cache *>(self);
     unsigned long long cfg, pools, ws;
     if (!PyArg_ParseTuple(args, "KKKKi", &cfg, &pools, &ws, &c->ws_bytes, &c->index)) return -1;
+    if (!cfg || !pools) {
+        PyErr_SetString(PyExc_ValueError, "Cache: no configuration or no pools");
+        return -1;
+    }
     c->cfg = *reinterpret_cast<const spava_cache_config *>(cfg);
     c->pools = *reinterpret_cast<const spava_cache_pools *>(pools);
     c->ws = reinterpret_cast<void *>(ws);

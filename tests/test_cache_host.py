@@ -207,3 +207,36 @@ def test_quantiser_against_every_e4m3_value():
         near = dist == best[:, None]
         even = near & ((half % 2 == 0)[None] | (near.sum(1) == 1)[:, None])
         assert torch.equal(vals[even.double().argmax(1)], z[i])
+
+
+def test_package_imports_before_its_extensions_are_built(tmp_path):
+    """A fresh checkout can import the package, and so build it."""
+    import os
+    import shutil
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    shutil.copytree(os.path.join(root, "sequence_sparse_attention_b200"), tmp_path / "sequence_sparse_attention_b200",
+                    ignore=shutil.ignore_patterns("*.so", "__pycache__"))
+    shutil.copytree(os.path.join(root, "include"), tmp_path / "include")
+    code = ("import sequence_sparse_attention_b200 as s, sequence_sparse_attention_b200.build, sys\n"
+            "try:\n    s.cache._load_calls()\nexcept ImportError as e:\n    sys.exit(0 if 'build it with' in str(e) else 1)\n"
+            "sys.exit(2)")
+    assert subprocess.run([sys.executable, "-c", code], cwd=tmp_path).returncode == 0
+
+
+def test_compiled_calls_load_without_a_gpu():
+    from sequence_sparse_attention_b200.cache import _load_calls
+    calls = _load_calls()
+    with pytest.raises(ValueError):
+        calls.Rope(0, 0, 0, 0, 0)
+    with pytest.raises(ValueError):
+        calls.Cache(0, 0, 0, 0, 0)
+    c = rope()
+    r = calls.Rope(ctypes.addressof(c), 0, 0, 0, 0)
+    with pytest.raises(TypeError):
+        r.apply(1)
+    x = torch.zeros(2, 4, 64, dtype=torch.bfloat16)
+    for bad in ((x, x, None, None, None), (1, x, None, None, None), (x[0], x, None, None, None)):
+        with pytest.raises(ValueError):      # host tensors, no tensor, no rows
+            r.apply(*bad)
