@@ -573,6 +573,48 @@ def test_a_chain_of_calls_without_waiting():
                 assert torch.equal(o, want[i % 4][0])
 
 
+def test_calls_wait_for_events_of_other_streams():
+    """Between two calls on one stream, an event of another stream on which what
+    the second call reads is still being made: the dependent launch waits for both."""
+    Hq, Hkv, d, page = 28, 4, 128, 16
+    for tokens in (16, 900, 1 << 16):             # tables for a warp, a cluster, the line
+        lens = [min(900, tokens)]
+        cache, pools, q, table, lt = attn_case(lens, Hq, Hkv, d, page, False, seed=41, extra=0, poison=False)
+        tb = widen(table, page, tokens) if tokens > 900 else table
+        q2 = q.flip(1).contiguous()
+        rows = randn(lens[0], Hkv, d, g=gen(2))
+        want = cache.attn(q2, tb, lt)
+        torch.cuda.synchronize()
+        a, b = torch.cuda.Stream(), torch.cuda.Stream()
+        qb = q.clone()
+        for _ in range(3):
+            qb.copy_(q)
+            torch.cuda.synchronize()
+            with torch.cuda.stream(a):
+                torch.cuda._sleep(5_000_000)      # a few ms
+                qb.copy_(q2)
+                made = a.record_event()
+            with torch.cuda.stream(b):
+                cache.read(tb, lt, lens[0])
+                cache.attn(q, tb, lt)
+                b.wait_event(made)
+                got = cache.attn(qb, tb, lt)
+            b.synchronize()
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        # and the other way: a later kernel of another stream waits for the last call
+        other = PagedCache(cache.lay, k_pages=pools[0].clone(), v_pages=pools[1].clone())
+        with torch.cuda.stream(a):
+            torch.cuda._sleep(5_000_000)
+            other.write(rows, rows, tb, lt)
+            k, v = other.read(tb, lt, lens[0])
+            done = a.record_event()
+        b.wait_event(done)
+        with torch.cuda.stream(b):
+            copy = k.clone()
+        b.synchronize()
+        assert torch.equal(copy[0], rows)
+
+
 def test_threads_share_a_cache():
     """Calls from several host threads, each on its own stream with its own workspace."""
     import threading
