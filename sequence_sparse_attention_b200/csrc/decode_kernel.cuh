@@ -99,9 +99,10 @@ __device__ __forceinline__ float exp2_approx(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t *>(&h);
+__device__ __forceinline__ uint32_t half2_bits(const __half2 &h) { return *reinterpret_cast<const uint32_t *>(&h); }
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) { return half2_bits(__floats2half2_rn(lo, hi)); }
+__device__ __forceinline__ uint32_t scale_half2(uint32_t a, float f) {
+    return half2_bits(__hmul2(*reinterpret_cast<const __half2 *>(&a), __float2half2_rn(f)));
 }
 
 __device__ __forceinline__ void cluster_sync() {
@@ -136,6 +137,12 @@ __device__ __forceinline__ void add_part(float4 &o, const float4 &y, float f) {
 // O = sum 2^(s + e - m) v with e the value's exponent (m = lm where there is
 // none).  kDecNone marks a part without a finite score.
 constexpr float kDecNone = -3.402823466e38f;
+// How far a score may pass its reference before that follows.
+constexpr float kDecLag = 8.f;
+// e4m3: m lies this far below the largest s + e, as fp16 holds weights of up to
+// 2^(kDecLift + kDecLag) and small ones need its range downwards.  What the rounding
+// to fp16 leaves of a weight enters by a second product, kDecLow times as large.
+constexpr float kDecLift = 7.f, kDecLow = 2048.f;
 
 __device__ __forceinline__ void store_lse(const DecodeParams &p, int b, int head, float lm, float l) {
     if (p.lse)
@@ -170,6 +177,11 @@ struct DecodeShape {
     static constexpr int KS = D / 16;                      // k steps of a score
     static constexpr int MT = D / 16;                      // 16-row tiles of O^T
     static constexpr int HEADS = 8 * NT;
+    // The low products of an e4m3 cache have accumulators of their own where the
+    // registers hold them; else the values are made kDecLow times smaller for them,
+    // which is exact in fp16 (512 sequences of 2000 tokens, 4 heads a KV head: 326 us,
+    // 348 with smaller values; two tiles of heads would spill).
+    static constexpr bool APART = E4M3 && NT == 1;
     // The 16-byte pieces of a row lie permuted (piece ^ swizzle) so that the
     // eight lanes that read at a time, pieces c of the K rows g, g + 1 or pieces
     // g, g + 1 of the V rows 2c, meet all banks.
@@ -213,10 +225,12 @@ struct DecodeShape {
 //     passes that.  Sums and O stay in fp32.
 //   - bf16: P enters as hi + lo, two bf16 products, 16 significant bits: one
 //     bf16 rounding of P would cost as much as the rounding of the output.
-//     e4m3: K, V, P and the scaled q are fp16 (e4m3 is exact in it, P keeps 11
-//     bits).  A row's scales come in as exponents: of K into the score, of V
-//     into P, whose reference m then covers score + exponent, while the sum l
-//     has its own, lm.
+//     e4m3: K, V and the scaled q are fp16 (e4m3 is exact in it) and P two fp16
+//     products, 22 significant bits down to 2^-25 of the largest weight and steps of
+//     2^-42 of it below.  A row's scales come in as exponents: of K into the score,
+//     of V into P, whose reference m then covers score + exponent, while the sum
+//     l has its own, lm.  (One product, 11 bits: 512 sequences of 2000 tokens 320
+//     instead of 326 us.)
 //   - The work of the whole batch is a line of units (BLOCK tokens of one
 //     sequence and KV head), cut into equal shares, one per block, by every
 //     block for itself from the lengths: long and short sequences balance, and
@@ -224,7 +238,7 @@ struct DecodeShape {
 //     of cut items in the workspace for join_kernel.
 //
 // Measured: 131072 tokens, 28/4 heads of 128, bf16, 48.0 us with the join, 5.6 TB/s;
-// 512 sequences of 2000 tokens, 32/8 heads, e4m3, 322 us, the copy rate.
+// 512 sequences of 2000 tokens, 32/8 heads, e4m3, 327 us.
 template <int D, bool E4M3, int NT, DecodeMode MODE>
 __device__ __forceinline__ void decode_body(const DecodeParams &p) {
     using S = DecodeShape<D, E4M3, NT>;
@@ -378,14 +392,14 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
             }
         }
 
-        float acc[NT][S::MT][4];
+        float acc[NT][S::MT][4], acc_low[S::MT][4];
         float m_ref[NT][2], l_ref[NT][2], l_sum[NT][2];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
 #pragma unroll
             for (int i = 0; i < S::MT; ++i)
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[t][i][k] = 0.f;
+                for (int k = 0; k < 4; ++k) acc[t][i][k] = acc_low[i][k] = 0.f;
 #pragma unroll
             for (int k = 0; k < 2; ++k) m_ref[t][k] = l_ref[t][k] = kDecNone, l_sum[t][k] = 0.f;
         }
@@ -480,8 +494,8 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
                         x *= q_scale[t][k % 2];
                         if (!((bits >> (g + 8 * (k / 2))) & 1)) x = -INFINITY;
                         s[sb][t][k] = x;
-                        grow |= x > l_ref[t][k % 2] + 8.f;
-                        if (E4M3) grow |= x + v_exp[sb][k / 2] > m_ref[t][k % 2] + 8.f;
+                        grow |= x > l_ref[t][k % 2] + kDecLag;
+                        if (E4M3) grow |= x + v_exp[sb][k / 2] > m_ref[t][k % 2] + (kDecLift + kDecLag);
                     }
             }
             // ---- a new reference, where a score passed the old one by 2^8
@@ -496,7 +510,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
 #pragma unroll
                             for (int y = 0; y < 2; ++y) {
                                 lm = fmaxf(lm, s[sb][t][2 * y + k]);
-                                if (E4M3) m = fmaxf(m, s[sb][t][2 * y + k] + v_exp[sb][y]);
+                                if (E4M3) m = fmaxf(m, s[sb][t][2 * y + k] + v_exp[sb][y] - kDecLift);
                             }
 #pragma unroll
                         for (int o = 4; o < 32; o <<= 1) {
@@ -509,7 +523,10 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
                         m_ref[t][k] = m;
                         l_ref[t][k] = lm;
 #pragma unroll
-                        for (int d = 0; d < S::MT; ++d) acc[t][d][k] *= f, acc[t][d][2 + k] *= f;
+                        for (int d = 0; d < S::MT; ++d) {
+                            acc[t][d][k] *= f, acc[t][d][2 + k] *= f;
+                            if (S::APART) acc_low[d][k] *= f, acc_low[d][2 + k] *= f;
+                        }
                     }
             }
             // ---- O^T += V^T P^T
@@ -529,7 +546,10 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
                             w[k] = E4M3 ? exp2_approx(x + v_exp[sb][y] - m_ref[t][k]) : pr;
                         }
                         if (E4M3) {
-                            hi[t][y] = movmatrix_trans(pack_half2(w[0], w[1]));
+                            const __half2 h = __floats2half2_rn(w[0], w[1]);
+                            const float2 hf = __half22float2(h);
+                            hi[t][y] = movmatrix_trans(half2_bits(h));
+                            lo[t][y] = movmatrix_trans(pack_half2((w[0] - hf.x) * kDecLow, (w[1] - hf.y) * kDecLow));
                         } else {
                             const uint32_t h = bf_pack(w[0], w[1]);
                             hi[t][y] = movmatrix_trans(h);
@@ -562,6 +582,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
                     }
                 } else {
                     constexpr int W = S::VB / 4;  // words of four d's
+                    auto low = [](uint32_t a) { return S::APART ? a : scale_half2(a, 1.f / kDecLow); };
                     uint32_t v[4][W];
 #pragma unroll
                     for (int y = 0; y < 4; ++y) {
@@ -593,6 +614,14 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
                             mma16816<true>(acc[t][2 * w], a00, a01, a02, a03, hi[t][0], hi[t][1]);
                             mma16816<true>(acc[t][2 * w + 1], a10, a11, a12, a13, hi[t][0], hi[t][1]);
                         }
+                        const uint32_t b00 = low(a00), b01 = low(a01), b02 = low(a02), b03 = low(a03);
+                        const uint32_t b10 = low(a10), b11 = low(a11), b12 = low(a12), b13 = low(a13);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t) {
+                            float(&to)[S::MT][4] = S::APART ? acc_low : acc[t];
+                            mma16816<true>(to[2 * w], b00, b01, b02, b03, lo[t][0], lo[t][1]);
+                            mma16816<true>(to[2 * w + 1], b10, b11, b12, b13, lo[t][0], lo[t][1]);
+                        }
                     }
                 }
             }
@@ -603,6 +632,11 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
             stage = stage == kDecStages - 1 ? 0 : stage + 1;
         }
         cp_async_wait<0>();
+        if (S::APART)
+#pragma unroll
+            for (int i = 0; i < S::MT; ++i)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[0][i][k] = fmaf(acc_low[i][k], 1.f / kDecLow, acc[0][i][k]);
 
         if (MODE == DecodeMode::kWarp) {
 #pragma unroll

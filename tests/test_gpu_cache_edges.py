@@ -1,0 +1,105 @@
+"""The answering side at the edges of its ranges: small softmax weights of a
+quantised cache."""
+import math
+
+import pytest
+import torch
+
+import cache_util as cu
+from cache_util import E4M3
+from sequence_sparse_attention_b200 import CacheLayout, PagedCache
+
+pytestmark = pytest.mark.gpu
+
+BF16 = torch.bfloat16
+
+
+def gen(seed=0):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def randn(*shape, g, scale=1.0):
+    return (torch.randn(shape, generator=g, device="cuda") * scale).to(BF16)
+
+
+def lengths(*lens):
+    return torch.tensor(lens, dtype=torch.int32, device="cuda")
+
+
+# ------------------------------------------------------------------ weights of a quantised cache
+def check_weights(o, q, pools, table, lens, page):
+    """One-token attention over an e4m3 cache, whose weights enter as two fp16.
+
+    Bound, with A = sum_t p_t |v_t| and one element's half step of bf16, 2^(floor
+    log2 |o| - 8), for the output's rounding:
+      * the score: d products and additions in fp32, each off by at most 2^-23 of
+        the partial sums' bound sum |q_i k_i|, four scalings of 2^-24, and q's
+        fp16 below 2^-24 of the head's largest (half a step of it, 2^-25); a
+        weight is off by twice that, numerator and sum;
+      * the exponential: 2^-21 of it, and its fp32 argument by 2^-24 of |s| / ln 2,
+        taken twice (sum and weight): in ds as 2 * 2^-24 |s|;
+      * the weight as hi + lo: 2^-22, and below fp16's normal range half a step,
+        2^-25, of a unit that is 2^18 times smaller than the reference, which is
+        no larger than the largest p_t 2^e_t: with |v| <= 448 2^e and max|v_t| >
+        224 2^e_t, 2^-43 * 2 of the largest p_t max|v_t| a token;
+      * two MMAs of 16 tokens each and the joins: (2 m / 16 + 64) * 2^-23 of A,
+        the sum of the weights as much."""
+    n, Hq, d = q.shape
+    Hkv = pools[0].shape[1]
+    scale = 1 / math.sqrt(d)
+    for b, m in enumerate(lens):
+        k, v = cu.rows_of(pools, table, b, m, page)
+        for h in range(Hq):
+            kk, vv, qb = k[:, h * Hkv // Hq], v[:, h * Hkv // Hq], q[b, h].double()
+            s = scale * (kk @ qb)
+            mag = scale * (kk.abs() @ qb.abs())
+            ds = (d + 4) * 2.0 ** -23 * mag + 2.0 ** -25 * scale * qb.abs().max() * kk.abs().sum(-1) + 2 * 2.0 ** -24 * s.abs()
+            p = torch.softmax(s, 0)
+            want, A = p @ vv, p @ vv.abs()
+            # keys that carry no weight do not move the result: their ds counts with their weight
+            rel = 2.0 ** -20 + 2.0 ** -22 + 2 * (2 * m / 16 + 64) * 2.0 ** -23
+            err = rel * A + 2 * (p * ds) @ vv.abs() + (p @ ds) * 2 * want.abs()
+            err = err + 2.0 ** -43 * (p * vv.abs().amax(-1)).max() * 2 * m
+            half = torch.exp2(torch.floor(torch.log2(want.abs() + err)) - 8)
+            off = (o[b, h].double() - want).abs()
+            worst = float((off / (half + err)).max())
+            assert worst <= 1, (b, h, m, worst)
+
+
+@pytest.mark.parametrize("tokens,at,rows", [(600, 3, 1), (4000, 3999, 1), (131072, 70000, 1), (30000, 5, 300)])
+def test_small_weights_of_a_quantised_cache(tokens, at, rows):
+    """One key 18 nats above the rest, whose value is zero in every other column:
+    there the output is what the others leave, each with a weight of 2^-26.  Many
+    rows of the batch (over the same pages): each is one block's, with one reference."""
+    Hq, Hkv, d, page = 2, 1, 64, 64
+    g = gen(tokens + at)
+    k, v = randn(tokens, Hkv, d, g=g, scale=0.05), randn(tokens, Hkv, d, g=g).abs()
+    q = randn(rows, Hq, d, g=g)
+    q[..., 0] = 8.0
+    k[:, 0, 0] = 0
+    k[at, 0] = 0
+    k[at, 0, 0] = 18.0
+    v[at, :, ::2] = 0
+    pages = -(-tokens // page)
+    cache = PagedCache(CacheLayout(Hq, Hkv, d, page_size=page, n_pages=pages, dtype=E4M3))
+    table = cu.make_table(1, pages, pages, g)
+    cache.write(k, v, table, lengths(tokens))
+    o, _ = cache.attn(q, table.expand(rows, -1).contiguous(), lengths(*[tokens] * rows))
+    assert cache.device_status() == 0
+    some = sorted({0, rows // 2, rows - 1})
+    check_weights(o[some], q[some], cache.tensors, table.expand(len(some), -1), [tokens] * len(some), page)
+
+
+@pytest.mark.parametrize("Hq,Hkv,d", [(32, 8, 128), (4, 2, 64), (24, 2, 128), (16, 1, 64)])
+@pytest.mark.parametrize("tokens", [2, 40, 300])
+def test_weights_of_a_quantised_cache_keep_their_bits(Hq, Hkv, d, tokens):
+    """Ordinary contexts: the output is the 64-bit one, rounded once."""
+    page, n = 16, 24
+    g = gen(tokens)
+    pages = -(-tokens // page)
+    pools = cu.make_pools(n * pages, Hkv, page, d, True, g)
+    cache = PagedCache(CacheLayout(Hq, Hkv, d, page_size=page, n_pages=n * pages, dtype=E4M3),
+                       k_pages=pools[0], v_pages=pools[1], k_exp=pools[2], v_exp=pools[3])
+    table, q = cu.make_table(n, pages, n * pages, g), randn(n, Hq, d, g=g)
+    o, _ = cache.attn(q, table, lengths(*[tokens] * n))
+    check_weights(o, q, pools, table, [tokens] * n, page)
