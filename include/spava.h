@@ -420,9 +420,10 @@ typedef struct {
  * [n_seqs], the tokens of each sequence, new ones included.  max_pages >= 1,
  * max_pages * page_size <= 2^31 - 2^16, n_seqs < 2^20.  Table entries behind the last
  * page of a sequence may hold anything.  Sequences may share pages.  A length below
- * 0 counts as 0, one beyond the table as the table's end; a page outside the
- * pool is neither read nor written, its positions count as absent; each of the
- * three sets bit 1 of the workspace status word. */
+ * 0 counts as 0; of one beyond the table, what lies behind the table is neither
+ * read nor written; a page outside the pool is neither read nor written, its
+ * positions count as absent; each of the three sets bit 1 of the workspace status
+ * word. */
 typedef struct {
     int64_t n_seqs;
     int64_t max_pages;
@@ -438,7 +439,7 @@ spava_status spava_cache_workspace_size(const spava_cache_config *cfg, size_t *b
 
 /* Writes new_rows rows of every sequence, its last ones: row i of sequence b
  * (token b * new_rows + i of k and v) goes to position lens[b] - new_rows + i;
- * rows whose position would be negative are skipped.  k, v: [n_seqs *
+ * rows whose position would be negative, or lies behind the table, are skipped.  k, v: [n_seqs *
  * new_rows, Hkv, d] bf16, tokens k_stride and v_stride elements apart (as in
  * spava_qk_norm_rope).  Two rows that go to one place of the pool leave
  * unspecified contents there.  Nothing else in the pools changes. */

@@ -38,12 +38,16 @@ struct RowParams {
     FastDiv new_rows;
 };
 
-// Pool row of KV head 0 of a token row, kNoRow if it has no place.
+// Pool row of KV head 0 of a token row, kNoRow if it has no place.  Places count
+// back from the length as it is given: from the table's end, the rows of a sequence
+// that has outgrown it would fall on those that it holds.
 __device__ __forceinline__ uint32_t row_slot(const RowParams &p, uint32_t row) {
     uint32_t i;
     const uint32_t b = p.new_rows.quot(row, i);
-    const int pos = cache_len(p.cache, b) - static_cast<int>(p.new_rows.d) + static_cast<int>(i);
-    return pos >= 0 ? cache_row(p.cache, b, pos) : kNoRow;
+    const int n = p.cache.lens[b], len = fit_len(p.cache, n);
+    if (n < 0) return kNoRow;
+    const int pos = n - static_cast<int>(p.new_rows.d) + static_cast<int>(i);
+    return pos >= 0 && pos < len ? cache_row(p.cache, b, pos) : kNoRow;
 }
 
 __device__ __forceinline__ float2 fmul2(float2 a, float2 b) {

@@ -1,5 +1,5 @@
 """The answering side at the edges of its ranges: small softmax weights of a
-quantised cache."""
+quantised cache, lengths beyond the table."""
 import math
 
 import pytest
@@ -7,7 +7,7 @@ import torch
 
 import cache_util as cu
 from cache_util import E4M3
-from sequence_sparse_attention_b200 import CacheLayout, PagedCache
+from sequence_sparse_attention_b200 import CacheLayout, PagedCache, QKNormRope, RopeLayout
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +103,45 @@ def test_weights_of_a_quantised_cache_keep_their_bits(Hq, Hkv, d, tokens):
     table, q = cu.make_table(n, pages, n * pages, g), randn(n, Hq, d, g=g)
     o, _ = cache.attn(q, table, lengths(*[tokens] * n))
     check_weights(o, q, pools, table, [tokens] * n, page)
+
+
+# ------------------------------------------------------------------ lengths beyond the table
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("over,new", [(1, 1), (3, 1), (3, 5), (1, 40), (2 ** 31 - 1, 5), (-7, 2)])
+def test_rows_beyond_the_table_are_skipped(over, new, kind):
+    """A sequence that grows past its table keeps what it holds: rows whose
+    position is behind the table go nowhere, those before it to their place."""
+    Hq, Hkv, d, page, per = 4, 2, 64, 8, 4
+    cap, n = page * per, 3
+    g = gen(new)
+    pools = cu.make_pools(n * per, Hkv, page, d, kind == "e4m3", g)
+    cache = PagedCache(CacheLayout(Hq, Hkv, d, page_size=page, n_pages=n * per, dtype=pools[0].dtype),
+                       k_pages=pools[0], v_pages=pools[1], k_exp=pools[2], v_exp=pools[3])
+    table = cu.make_table(n, per, n * per, g)
+    raw = [20, min(cap + over, 2 ** 31 - 1) if over > 0 else over, cap]
+    q, k, v = randn(n * new, Hq, d, g=g), randn(n * new, Hkv, d, g=g), randn(n * new, Hkv, d, g=g)
+    want = [x if x is None else x.double() for x in pools]
+    for i, x in enumerate((k, v)):
+        vals, exps = cu.quantise(x) if kind == "e4m3" else (x.double(), None)
+        for b in range(n):
+            for r in range(new):
+                pos = raw[b] - new + r
+                if not 0 <= pos < cap:
+                    continue
+                p, at = cu.place(table, page, b, pos)
+                want[i][p, :, at] = vals[b * new + r]
+                if exps is not None:
+                    want[2 + i][p, :, at] = exps[b * new + r]
+    rope = QKNormRope(RopeLayout(Hq, Hkv, d, rope_dim=0, norm=False), device="cuda")
+    before = [x if x is None else x.view(torch.uint8).clone() for x in pools]
+    for call in ("write", "append"):
+        for x, was in zip(pools, before):
+            if x is not None:
+                x.view(torch.uint8).copy_(was)
+        if call == "write":
+            cache.write(k, v, table, lengths(*raw))
+        else:
+            assert torch.equal(cache.append(rope, q, k, v, None, table, lengths(*raw)), q)
+        for got, ref in zip(pools, want):
+            assert got is None or torch.equal(got.double(), ref)
+        assert cache.device_status() == 2 and cache.device_status() == 0
