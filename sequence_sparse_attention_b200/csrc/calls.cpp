@@ -76,20 +76,35 @@ at::Tensor output(PyObject *given, at::IntArrayRef shape, at::ScalarType type, i
     return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(index)), std::nullopt);
 }
 
-void *ptr(const at::Tensor &t) { return t.data_ptr(); }
+// Raises for a tensor without memory of its own (a transform's or a fake one).
+void *ptr(const at::Tensor &t, const char *name) {
+    void *p = t.data_ptr();
+    if (!t.storage().device().is_cuda()) throw Refused{c10::str(name, ": expected a tensor with memory, got ", said(t))};
+    return p;
+}
 
 // ------------------------------------------------------------------ calls
 PyObject *g_failed = nullptr;  // (function name, status): raises
 
+class WithoutGil {  // until it is destroyed, also by an exception
+    PyThreadState *state_ = PyEval_SaveThread();
+
+  public:
+    WithoutGil() = default;
+    WithoutGil(const WithoutGil &) = delete;
+    ~WithoutGil() { PyEval_RestoreThread(state_); }
+};
+
+// f(stream), the library call, without the GIL: it touches no Python object and no
+// tensor, whose addresses are taken before (and may raise).
 template <typename F>
 bool called(const char *name, int index, F f) {
     spava_status rc;
     {
         c10::cuda::CUDAGuard guard(static_cast<c10::DeviceIndex>(index));
         void *stream = c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(index)).stream();
-        Py_BEGIN_ALLOW_THREADS;
+        WithoutGil released;
         rc = f(stream);
-        Py_END_ALLOW_THREADS;
     }
     if (rc == SPAVA_OK) return true;
     if (!g_failed) {
@@ -172,7 +187,7 @@ const int32_t *positions_of(const Rope *r, PyObject *o, int64_t rows) {
     if (t.scalar_type() != at::kInt || !shaped || !on(t, r->index) || !t.is_contiguous())
         throw Refused{c10::str("positions: expected contiguous Int [", axes, ", ", rows, "] on cuda:", r->index, ", got ",
                                said(t))};
-    return static_cast<const int32_t *>(ptr(t));
+    return static_cast<const int32_t *>(ptr(t, "positions"));
 }
 
 // apply(q, k, positions, q_out, k_out)
@@ -188,9 +203,11 @@ PyObject *rope_apply(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         const int32_t *pos = positions_of(r, a[2], rows);
         const at::Tensor qo = output(a[3], q.sizes(), at::kBFloat16, r->index, "q_out");
         const at::Tensor ko = output(a[4], k.sizes(), at::kBFloat16, r->index, "k_out");
+        const void *qp = ptr(q, "q"), *kp = ptr(k, "k");
+        void *qop = ptr(qo, "q_out"), *kop = ptr(ko, "k_out");
         if (!called("spava_qk_norm_rope", r->index, [&](void *stream) {
-                return spava_qk_norm_rope(&c, rows, ptr(q), qs, ptr(k), ks, r->q_weight, r->k_weight, r->inv_freq, pos,
-                                          ptr(qo), ptr(ko), stream);
+                return spava_qk_norm_rope(&c, rows, qp, qs, kp, ks, r->q_weight, r->k_weight, r->inv_freq, pos, qop, kop,
+                                          stream);
             }))
             return nullptr;
         return pair(qo, THPVariable_Wrap(ko));
@@ -238,7 +255,7 @@ Space space_of(const Cache *c, PyObject *given) {
     const at::Tensor &t = tensor(given, "workspace");
     if (t.scalar_type() != at::kByte || !on(t, c->index) || !t.is_contiguous())
         throw Refused{c10::str("workspace: expected contiguous Byte on cuda:", c->index, ", got ", said(t))};
-    return {ptr(t), static_cast<size_t>(t.numel())};
+    return {ptr(t, "workspace"), static_cast<size_t>(t.numel())};
 }
 
 spava_cache_batch batch_of(const Cache *c, PyObject *table, PyObject *lens) {
@@ -247,7 +264,7 @@ spava_cache_batch batch_of(const Cache *c, PyObject *table, PyObject *lens) {
         t.size(0) != l.size(0) || !on(t, c->index) || !on(l, c->index) || !t.is_contiguous() || !l.is_contiguous())
         throw Refused{c10::str("table, lens: expected contiguous Int [sequences, max_pages] and [sequences] on cuda:",
                                c->index, ", got ", said(t), " and ", said(l))};
-    return {t.size(0), t.size(1), static_cast<const int32_t *>(ptr(t)), static_cast<const int32_t *>(ptr(l))};
+    return {t.size(0), t.size(1), static_cast<const int32_t *>(ptr(t, "table")), static_cast<const int32_t *>(ptr(l, "lens"))};
 }
 
 // write(k, v, table, lens, workspace)
@@ -261,8 +278,9 @@ PyObject *cache_write(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         const int64_t ks = token_stride(k, rows, c->cfg.n_kv_heads, c->cfg.head_dim, c->index, "k");
         const int64_t vs = token_stride(v, rows, c->cfg.n_kv_heads, c->cfg.head_dim, c->index, "v");
         const Space s = space_of(c, a[4]);
+        const void *kp = ptr(k, "k"), *vp = ptr(v, "v");
         if (!called("spava_cache_write", c->index, [&](void *stream) {
-                return spava_cache_write(&c->cfg, &c->pools, &batch, fresh, ptr(k), ks, ptr(v), vs, s.ws, s.bytes, stream);
+                return spava_cache_write(&c->cfg, &c->pools, &batch, fresh, kp, ks, vp, vs, s.ws, s.bytes, stream);
             }))
             return nullptr;
         Py_RETURN_NONE;
@@ -287,9 +305,11 @@ PyObject *cache_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         const int32_t *pos = positions_of(r, a[4], rows);
         const Space s = space_of(c, a[8]);
         const at::Tensor qo = output(a[7], q.sizes(), at::kBFloat16, c->index, "q_out");
+        const void *qp = ptr(q, "q"), *kp = ptr(k, "k"), *vp = ptr(v, "v");
+        void *qop = ptr(qo, "q_out");
         if (!called("spava_cache_append", c->index, [&](void *stream) {
-                return spava_cache_append(&r->cfg, &c->cfg, &c->pools, &batch, fresh, ptr(q), qs, ptr(k), ks, ptr(v), vs,
-                                          r->q_weight, r->k_weight, r->inv_freq, pos, ptr(qo), s.ws, s.bytes, stream);
+                return spava_cache_append(&r->cfg, &c->cfg, &c->pools, &batch, fresh, qp, qs, kp, ks, vp, vs, r->q_weight,
+                                          r->k_weight, r->inv_freq, pos, qop, s.ws, s.bytes, stream);
             }))
             return nullptr;
         return THPVariable_Wrap(qo);
@@ -309,8 +329,9 @@ PyObject *cache_read(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         const Space s = space_of(c, a[6]);
         const at::Tensor ko = output(a[4], shape, at::kBFloat16, c->index, "k_out");
         const at::Tensor vo = output(a[5], shape, at::kBFloat16, c->index, "v_out");
+        void *kop = ptr(ko, "k_out"), *vop = ptr(vo, "v_out");
         if (!called("spava_cache_read", c->index, [&](void *stream) {
-                return spava_cache_read(&c->cfg, &c->pools, &batch, first, rows, ptr(ko), ptr(vo), s.ws, s.bytes, stream);
+                return spava_cache_read(&c->cfg, &c->pools, &batch, first, rows, kop, vop, s.ws, s.bytes, stream);
             }))
             return nullptr;
         return pair(ko, THPVariable_Wrap(vo));
@@ -333,9 +354,11 @@ PyObject *cache_attn(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         if (want < 0) return nullptr;
         at::Tensor lse;
         if (want || a[4] != Py_None) lse = output(a[4], lse_shape, at::kFloat, c->index, "lse");
+        const void *qp = ptr(q, "q");
+        void *op = ptr(o, "o");
+        float *lp = lse.defined() ? static_cast<float *>(ptr(lse, "lse")) : nullptr;
         if (!called("spava_cache_attn", c->index, [&](void *stream) {
-                return spava_cache_attn(&c->cfg, &c->pools, &batch, ptr(q), ptr(o),
-                                        lse.defined() ? static_cast<float *>(ptr(lse)) : nullptr, s.ws, s.bytes, stream);
+                return spava_cache_attn(&c->cfg, &c->pools, &batch, qp, op, lp, s.ws, s.bytes, stream);
             }))
             return nullptr;
         return pair(o, lse.defined() ? THPVariable_Wrap(lse) : Py_NewRef(Py_None));

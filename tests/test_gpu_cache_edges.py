@@ -1,5 +1,5 @@
 """The answering side at the edges of its ranges: small softmax weights of a
-quantised cache, lengths beyond the table."""
+quantised cache, lengths beyond the table, tensors without an address."""
 import math
 
 import pytest
@@ -145,3 +145,26 @@ def test_rows_beyond_the_table_are_skipped(over, new, kind):
         for got, ref in zip(pools, want):
             assert got is None or torch.equal(got.double(), ref)
         assert cache.device_status() == 2 and cache.device_status() == 0
+
+
+# ------------------------------------------------------------------ tensors without an address
+def test_transforms_raise_and_leave_the_process_and_the_calls_alone():
+    Hq, Hkv, d, page = 4, 2, 64, 16
+    g = gen(7)
+    q, k = randn(3, 2, Hq, d, g=g), randn(3, 2, Hkv, d, g=g)
+    cache = PagedCache(CacheLayout(Hq, Hkv, d, page_size=page, n_pages=4))
+    rope = QKNormRope(RopeLayout(Hq, Hkv, d, rope_dim=0), device="cuda")
+    table, lens = cu.make_table(2, 2, 4, g), lengths(20, 30)
+    cache.write(k[0], k[1], table, lens)
+    want = cache.attn(q[0], table, lens)
+    for call in (lambda x, y: rope.apply(x, y), lambda x, y: cache.write(y, y, table, lens),
+                 lambda x, y: cache.append(rope, x, y, y, None, table, lens), lambda x, y: cache.attn(x, table, lens)):
+        with pytest.raises(RuntimeError):
+            torch.vmap(call)(q, k)
+        with pytest.raises(RuntimeError):
+            torch.func.jvp(lambda x: call(x, x[:, :Hkv]), (q[0],), (q[1],))
+    with pytest.raises(RuntimeError):
+        torch.vmap(lambda t: cache.read(t, lens, 4))(torch.stack([table] * 3))
+    cache.write(k[0], k[1], table, lens)
+    got = cache.attn(q[0], table, lens)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
