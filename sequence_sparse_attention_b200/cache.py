@@ -18,7 +18,7 @@ from dataclasses import dataclass
 import torch
 
 from . import native
-from .native import SpavaCacheConfig, SpavaCachePools, SpavaRopeConfig
+from .native import SpavaCacheConfig, SpavaRopeConfig
 
 _CACHE_TYPES = {torch.bfloat16: 0, torch.float8_e4m3fn: 1}
 
@@ -102,6 +102,12 @@ def _load_calls():
     return _calls
 
 
+def _kept(name):
+    """A tensor that the compiled calls keep.  Its contents and memory (``.data``) may
+    be replaced; another tensor takes another object."""
+    return property(lambda self: getattr(self._calls, name), doc=f"``{name}``, read-only.")
+
+
 class QKNormRope:
     """RMS norm of every query and key head and their rotation, in one launch.
     ``inv_freq``: float32 [rope_dim / 2], radians per position; ``q_weight``,
@@ -119,9 +125,9 @@ class QKNormRope:
         for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
             if t is not None:
                 _check(t, (lay.d,), torch.bfloat16, index, name)
-        self.inv_freq, self.q_weight, self.k_weight = inv_freq, q_weight, k_weight
-        self._calls = _load_calls().Rope(ctypes.addressof(self.cfg), *(0 if t is None else t.data_ptr()
-                                                                for t in (q_weight, k_weight, inv_freq)), index)
+        self._calls = _load_calls().Rope(ctypes.addressof(self.cfg), q_weight, k_weight, inv_freq, index)
+
+    q_weight, k_weight, inv_freq = _kept("q_weight"), _kept("k_weight"), _kept("inv_freq")
 
     def apply(self, q, k, positions=None, q_out=None, k_out=None):
         """q [rows, Hq, d], k [rows, Hkv, d] (views of one projection are fine),
@@ -155,20 +161,18 @@ class PagedCache:
             _check(t, shape, dtype, index, name)
             return t
 
-        self.k_pages = pool(k_pages, shape, lay.dtype, "k_pages")
-        self.v_pages = pool(v_pages, shape, lay.dtype, "v_pages")
-        self.k_exp = self.v_exp = None
+        k_pages = pool(k_pages, shape, lay.dtype, "k_pages")
+        v_pages = pool(v_pages, shape, lay.dtype, "v_pages")
         if self.cfg.type == 1:
-            self.k_exp = pool(k_exp, shape[:3], torch.int8, "k_exp")
-            self.v_exp = pool(v_exp, shape[:3], torch.int8, "v_exp")
+            k_exp = pool(k_exp, shape[:3], torch.int8, "k_exp")
+            v_exp = pool(v_exp, shape[:3], torch.int8, "v_exp")
         elif k_exp is not None or v_exp is not None:
             raise ValueError("k_exp, v_exp: only a torch.float8_e4m3fn cache has them")
-        self.workspace = self.new_workspace() if workspace is None else workspace
-        _check(self.workspace, (self.workspace.numel(),), torch.uint8, index, "workspace")
-        pools = SpavaCachePools(*(None if t is None else t.data_ptr()
-                                  for t in (self.k_pages, self.v_pages, self.k_exp, self.v_exp)))
-        self._calls = _load_calls().Cache(ctypes.addressof(self.cfg), ctypes.addressof(pools), self.workspace.data_ptr(),
-                                   self.workspace.numel(), index)
+        workspace = self.new_workspace() if workspace is None else workspace
+        _check(workspace, (workspace.numel(),), torch.uint8, index, "workspace")
+        self._calls = _load_calls().Cache(ctypes.addressof(self.cfg), (k_pages, v_pages), (k_exp, v_exp), workspace, index)
+
+    k_pages, v_pages, k_exp, v_exp, workspace = map(_kept, ("k_pages", "v_pages", "k_exp", "v_exp", "workspace"))
 
     @property
     def tensors(self):

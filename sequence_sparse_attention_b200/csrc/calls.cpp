@@ -7,6 +7,7 @@
 // Argument marshalling only, like api.py: the computation is libspava's.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
+#include <structmember.h>
 
 #include <ATen/ATen.h>
 #include <ATen/cuda/EmptyTensor.h>
@@ -152,30 +153,86 @@ PyObject *pair(const at::Tensor &a, PyObject *b) {  // steals b
     return t;
 }
 
+// ------------------------------------------------------------------ kept tensors
+// Both objects keep Python tensors, not addresses: a tensor's memory may be
+// replaced (``weight.data = ...``, a module that moves), so every call checks it
+// and takes its address anew.
+// A constructor's tensor as a new reference; null for None or 0.
+bool kept(PyObject *o, PyObject **to, const char *name) {
+    if (o == Py_None || (PyLong_Check(o) && PyObject_IsTrue(o) == 0)) {
+        Py_CLEAR(*to);
+        return true;
+    }
+    if (!THPVariable_Check(o)) {
+        PyErr_Format(PyExc_ValueError, "%s: expected a tensor, got %s", name, Py_TYPE(o)->tp_name);
+        return false;
+    }
+    Py_INCREF(o);
+    Py_XSETREF(*to, o);
+    return true;
+}
+
+void *kept_ptr(PyObject *o, at::IntArrayRef shape, at::ScalarType type, int index, const char *name) {
+    if (!o) return nullptr;
+    const at::Tensor &t = THPVariable_Unpack(o);
+    check(t, shape, type, index, name);
+    return ptr(t, name);
+}
+
+// T: {PyObject_HEAD; PyObject *tensors[N]; ...}
+template <typename T>
+int visit_kept(PyObject *self, visitproc visit, void *arg) {
+    for (PyObject *o : reinterpret_cast<T *>(self)->tensors) Py_VISIT(o);
+    return 0;
+}
+template <typename T>
+int clear_kept(PyObject *self) {
+    for (PyObject *&o : reinterpret_cast<T *>(self)->tensors) Py_CLEAR(o);
+    return 0;
+}
+template <typename T>
+void dealloc(PyObject *self) {
+    PyObject_GC_UnTrack(self);
+    clear_kept<T>(self);
+    Py_TYPE(self)->tp_free(self);
+}
+#define SPAVA_KEPT(type, name, i) \
+    {name, T_OBJECT, offsetof(type, tensors) + (i) * sizeof(PyObject *), READONLY, nullptr}
+
 // ------------------------------------------------------------------ Rope
-// The tables' memory is the Python object's, which holds this one.
 struct Rope {
     PyObject_HEAD
+    PyObject *tensors[3];  // q_weight, k_weight, inv_freq
     spava_rope_config cfg;
-    const void *q_weight, *k_weight;
-    const float *inv_freq;
     int index;
 };
+PyMemberDef rope_members[] = {SPAVA_KEPT(Rope, "q_weight", 0), SPAVA_KEPT(Rope, "k_weight", 1),
+                              SPAVA_KEPT(Rope, "inv_freq", 2), {nullptr, 0, 0, 0, nullptr}};
 
-// (address of a spava_rope_config, q_weight, k_weight, inv_freq addresses, device)
+// (address of a spava_rope_config, q_weight, k_weight, inv_freq, device)
 int rope_init(PyObject *self, PyObject *args, PyObject *) {
     Rope *r = reinterpret_cast<Rope *>(self);
-    unsigned long long cfg, q, k, f;
-    if (!PyArg_ParseTuple(args, "KKKKi", &cfg, &q, &k, &f, &r->index)) return -1;
+    unsigned long long cfg;
+    PyObject *q, *k, *f;
+    if (!PyArg_ParseTuple(args, "KOOOi", &cfg, &q, &k, &f, &r->index)) return -1;
     if (!cfg) {
         PyErr_SetString(PyExc_ValueError, "Rope: no configuration");
         return -1;
     }
     r->cfg = *reinterpret_cast<const spava_rope_config *>(cfg);
-    r->q_weight = reinterpret_cast<const void *>(q);
-    r->k_weight = reinterpret_cast<const void *>(k);
-    r->inv_freq = reinterpret_cast<const float *>(f);
-    return 0;
+    return kept(q, &r->tensors[0], "q_weight") && kept(k, &r->tensors[1], "k_weight") &&
+                   kept(f, &r->tensors[2], "inv_freq") ? 0 : -1;
+}
+
+struct RopeTables {
+    const void *q_weight, *k_weight;
+    const float *inv_freq;
+};
+RopeTables tables_of(const Rope *r) {
+    const int64_t d = r->cfg.head_dim, half = r->cfg.rope_dim / 2;
+    return {kept_ptr(r->tensors[0], d, at::kBFloat16, r->index, "q_weight"),
+            kept_ptr(r->tensors[1], d, at::kBFloat16, r->index, "k_weight"),
+            half ? static_cast<const float *>(kept_ptr(r->tensors[2], half, at::kFloat, r->index, "inv_freq")) : nullptr};
 }
 
 const int32_t *positions_of(const Rope *r, PyObject *o, int64_t rows) {
@@ -205,8 +262,9 @@ PyObject *rope_apply(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         const at::Tensor ko = output(a[4], k.sizes(), at::kBFloat16, r->index, "k_out");
         const void *qp = ptr(q, "q"), *kp = ptr(k, "k");
         void *qop = ptr(qo, "q_out"), *kop = ptr(ko, "k_out");
+        const RopeTables w = tables_of(r);
         if (!called("spava_qk_norm_rope", r->index, [&](void *stream) {
-                return spava_qk_norm_rope(&c, rows, qp, qs, kp, ks, r->q_weight, r->k_weight, r->inv_freq, pos, qop, kop,
+                return spava_qk_norm_rope(&c, rows, qp, qs, kp, ks, w.q_weight, w.k_weight, w.inv_freq, pos, qop, kop,
                                           stream);
             }))
             return nullptr;
@@ -223,27 +281,46 @@ PyTypeObject RopeType = {PyVarObject_HEAD_INIT(nullptr, 0)};
 // ------------------------------------------------------------------ Cache
 struct Cache {
     PyObject_HEAD
+    PyObject *tensors[5];  // k_pages, v_pages, k_exp, v_exp, workspace
     spava_cache_config cfg;
-    spava_cache_pools pools;
-    void *ws;
-    unsigned long long ws_bytes;
     int index;
 };
+PyMemberDef cache_members[] = {SPAVA_KEPT(Cache, "k_pages", 0), SPAVA_KEPT(Cache, "v_pages", 1),
+                               SPAVA_KEPT(Cache, "k_exp", 2),   SPAVA_KEPT(Cache, "v_exp", 3),
+                               SPAVA_KEPT(Cache, "workspace", 4), {nullptr, 0, 0, 0, nullptr}};
 
-// (addresses of a spava_cache_config and a spava_cache_pools, of the workspace,
-// its bytes, device)
+// (address of a spava_cache_config, (k_pages, v_pages), (k_exp, v_exp), workspace, device)
 int cache_init(PyObject *self, PyObject *args, PyObject *) {
     Cache *c = reinterpret_cast<Cache *>(self);
-    unsigned long long cfg, pools, ws;
-    if (!PyArg_ParseTuple(args, "KKKKi", &cfg, &pools, &ws, &c->ws_bytes, &c->index)) return -1;
-    if (!cfg || !pools) {
+    unsigned long long cfg;
+    PyObject *pools, *exps, *ws;
+    if (!PyArg_ParseTuple(args, "KOOOi", &cfg, &pools, &exps, &ws, &c->index)) return -1;
+    if (!cfg || !PyTuple_Check(pools) || PyTuple_GET_SIZE(pools) != 2 || !PyTuple_Check(exps) ||
+        PyTuple_GET_SIZE(exps) != 2) {
         PyErr_SetString(PyExc_ValueError, "Cache: no configuration or no pools");
         return -1;
     }
     c->cfg = *reinterpret_cast<const spava_cache_config *>(cfg);
-    c->pools = *reinterpret_cast<const spava_cache_pools *>(pools);
-    c->ws = reinterpret_cast<void *>(ws);
-    return 0;
+    return kept(PyTuple_GET_ITEM(pools, 0), &c->tensors[0], "k_pages") &&
+                   kept(PyTuple_GET_ITEM(pools, 1), &c->tensors[1], "v_pages") &&
+                   kept(PyTuple_GET_ITEM(exps, 0), &c->tensors[2], "k_exp") &&
+                   kept(PyTuple_GET_ITEM(exps, 1), &c->tensors[3], "v_exp") && kept(ws, &c->tensors[4], "workspace")
+               ? 0
+               : -1;
+}
+
+spava_cache_pools pools_of(const Cache *c) {
+    const int64_t shape[4] = {c->cfg.n_pages, c->cfg.n_kv_heads, c->cfg.page_size, c->cfg.head_dim};
+    const at::IntArrayRef rows(shape, 3);
+    const bool e4m3 = c->cfg.type == SPAVA_CACHE_E4M3;
+    const at::ScalarType type = e4m3 ? at::kFloat8_e4m3fn : at::kBFloat16;
+    spava_cache_pools p{kept_ptr(c->tensors[0], shape, type, c->index, "k_pages"),
+                        kept_ptr(c->tensors[1], shape, type, c->index, "v_pages"), nullptr, nullptr};
+    if (e4m3) {
+        p.k_exp = static_cast<int8_t *>(kept_ptr(c->tensors[2], rows, at::kChar, c->index, "k_exp"));
+        p.v_exp = static_cast<int8_t *>(kept_ptr(c->tensors[3], rows, at::kChar, c->index, "v_exp"));
+    }
+    return p;
 }
 
 struct Space {
@@ -251,7 +328,8 @@ struct Space {
     size_t bytes;
 };
 Space space_of(const Cache *c, PyObject *given) {
-    if (given == Py_None) return {c->ws, static_cast<size_t>(c->ws_bytes)};
+    if (given == Py_None) given = c->tensors[4];
+    if (!given) return {nullptr, 0};
     const at::Tensor &t = tensor(given, "workspace");
     if (t.scalar_type() != at::kByte || !on(t, c->index) || !t.is_contiguous())
         throw Refused{c10::str("workspace: expected contiguous Byte on cuda:", c->index, ", got ", said(t))};
@@ -278,9 +356,10 @@ PyObject *cache_write(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         const int64_t ks = token_stride(k, rows, c->cfg.n_kv_heads, c->cfg.head_dim, c->index, "k");
         const int64_t vs = token_stride(v, rows, c->cfg.n_kv_heads, c->cfg.head_dim, c->index, "v");
         const Space s = space_of(c, a[4]);
+        const spava_cache_pools pools = pools_of(c);
         const void *kp = ptr(k, "k"), *vp = ptr(v, "v");
         if (!called("spava_cache_write", c->index, [&](void *stream) {
-                return spava_cache_write(&c->cfg, &c->pools, &batch, fresh, kp, ks, vp, vs, s.ws, s.bytes, stream);
+                return spava_cache_write(&c->cfg, &pools, &batch, fresh, kp, ks, vp, vs, s.ws, s.bytes, stream);
             }))
             return nullptr;
         Py_RETURN_NONE;
@@ -304,12 +383,14 @@ PyObject *cache_append(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         const int64_t vs = token_stride(v, rows, c->cfg.n_kv_heads, c->cfg.head_dim, c->index, "v");
         const int32_t *pos = positions_of(r, a[4], rows);
         const Space s = space_of(c, a[8]);
+        const spava_cache_pools pools = pools_of(c);
+        const RopeTables w = tables_of(r);
         const at::Tensor qo = output(a[7], q.sizes(), at::kBFloat16, c->index, "q_out");
         const void *qp = ptr(q, "q"), *kp = ptr(k, "k"), *vp = ptr(v, "v");
         void *qop = ptr(qo, "q_out");
         if (!called("spava_cache_append", c->index, [&](void *stream) {
-                return spava_cache_append(&r->cfg, &c->cfg, &c->pools, &batch, fresh, qp, qs, kp, ks, vp, vs, r->q_weight,
-                                          r->k_weight, r->inv_freq, pos, qop, s.ws, s.bytes, stream);
+                return spava_cache_append(&r->cfg, &c->cfg, &pools, &batch, fresh, qp, qs, kp, ks, vp, vs, w.q_weight,
+                                          w.k_weight, w.inv_freq, pos, qop, s.ws, s.bytes, stream);
             }))
             return nullptr;
         return THPVariable_Wrap(qo);
@@ -327,11 +408,12 @@ PyObject *cache_read(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         if (rows < 0 || first < 0) throw Refused{c10::str("rows, first: expected >= 0, got ", rows, " and ", first)};
         const int64_t shape[4] = {batch.n_seqs, rows, c->cfg.n_kv_heads, c->cfg.head_dim};
         const Space s = space_of(c, a[6]);
+        const spava_cache_pools pools = pools_of(c);
         const at::Tensor ko = output(a[4], shape, at::kBFloat16, c->index, "k_out");
         const at::Tensor vo = output(a[5], shape, at::kBFloat16, c->index, "v_out");
         void *kop = ptr(ko, "k_out"), *vop = ptr(vo, "v_out");
         if (!called("spava_cache_read", c->index, [&](void *stream) {
-                return spava_cache_read(&c->cfg, &c->pools, &batch, first, rows, kop, vop, s.ws, s.bytes, stream);
+                return spava_cache_read(&c->cfg, &pools, &batch, first, rows, kop, vop, s.ws, s.bytes, stream);
             }))
             return nullptr;
         return pair(ko, THPVariable_Wrap(vo));
@@ -348,6 +430,7 @@ PyObject *cache_attn(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         const int64_t shape[3] = {batch.n_seqs, c->cfg.n_q_heads, c->cfg.head_dim};
         check(q, shape, at::kBFloat16, c->index, "q");
         const Space s = space_of(c, a[6]);
+        const spava_cache_pools pools = pools_of(c);
         const at::Tensor o = output(a[3], shape, at::kBFloat16, c->index, "o");
         const int64_t lse_shape[2] = {c->cfg.n_q_heads, batch.n_seqs};
         const int want = PyObject_IsTrue(a[5]);
@@ -358,7 +441,7 @@ PyObject *cache_attn(PyObject *self, PyObject *const *a, Py_ssize_t n) {
         void *op = ptr(o, "o");
         float *lp = lse.defined() ? static_cast<float *>(ptr(lse, "lse")) : nullptr;
         if (!called("spava_cache_attn", c->index, [&](void *stream) {
-                return spava_cache_attn(&c->cfg, &c->pools, &batch, qp, op, lp, s.ws, s.bytes, stream);
+                return spava_cache_attn(&c->cfg, &pools, &batch, qp, op, lp, s.ws, s.bytes, stream);
             }))
             return nullptr;
         return pair(o, lse.defined() ? THPVariable_Wrap(lse) : Py_NewRef(Py_None));
@@ -383,14 +466,19 @@ PyObject *on_failure(PyObject *, PyObject *f) {
 PyMethodDef module_methods[] = {{"on_failure", on_failure, METH_O, nullptr}, {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_calls", nullptr, -1, module_methods};
 
-int add_type(PyObject *m, PyTypeObject &t, const char *name, const char *full, Py_ssize_t size, PyMethodDef *methods,
+template <typename T>
+int add_type(PyObject *m, PyTypeObject &t, const char *name, const char *full, PyMethodDef *methods, PyMemberDef *members,
              initproc init) {
     t.tp_name = full;
-    t.tp_basicsize = size;
-    t.tp_flags = Py_TPFLAGS_DEFAULT;
+    t.tp_basicsize = sizeof(T);
+    t.tp_flags = Py_TPFLAGS_DEFAULT | Py_TPFLAGS_HAVE_GC;
     t.tp_methods = methods;
+    t.tp_members = members;
     t.tp_init = init;
     t.tp_new = PyType_GenericNew;
+    t.tp_traverse = visit_kept<T>;
+    t.tp_clear = clear_kept<T>;
+    t.tp_dealloc = dealloc<T>;
     if (PyType_Ready(&t) < 0) return -1;
     return PyModule_AddObjectRef(m, name, reinterpret_cast<PyObject *>(&t));
 }
@@ -400,8 +488,8 @@ int add_type(PyObject *m, PyTypeObject &t, const char *name, const char *full, P
 PyMODINIT_FUNC PyInit__calls() {
     PyObject *m = PyModule_Create(&module);
     if (!m) return nullptr;
-    if (add_type(m, RopeType, "Rope", "_calls.Rope", sizeof(Rope), rope_methods, rope_init) < 0 ||
-        add_type(m, CacheType, "Cache", "_calls.Cache", sizeof(Cache), cache_methods, cache_init) < 0) {
+    if (add_type<Rope>(m, RopeType, "Rope", "_calls.Rope", rope_methods, rope_members, rope_init) < 0 ||
+        add_type<Cache>(m, CacheType, "Cache", "_calls.Cache", cache_methods, cache_members, cache_init) < 0) {
         Py_DECREF(m);
         return nullptr;
     }

@@ -6,7 +6,7 @@ import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
 
-from sequence_sparse_attention_b200 import RopeLayout
+from sequence_sparse_attention_b200 import CacheLayout, PagedCache, QKNormRope, RopeLayout
 from sequence_sparse_attention_b200.cache import _load_calls
 
 
@@ -28,3 +28,51 @@ def test_tensors_without_memory_are_refused(transform):
                 torch.func.grad(lambda x: rope.apply(x, k, pos, qo, ko)[0].float().sum())(q)
             else:
                 rope.apply(q, k, pos, qo, ko)
+
+
+# ------------------------------------------------------------------ kept tensors
+def test_kept_tensors_are_read_only():
+    """Another tensor in an attribute would not reach the calls: it is refused."""
+    for cls, names in ((QKNormRope, ("q_weight", "k_weight", "inv_freq")),
+                       (PagedCache, ("k_pages", "v_pages", "k_exp", "v_exp", "workspace"))):
+        for name in names:
+            assert isinstance(getattr(cls, name, None), property) and getattr(cls, name).fset is None
+
+
+def test_compiled_calls_keep_tensors_not_addresses():
+    """What a call uses is the tensor as it is then: one whose memory was replaced
+    by another type, shape or device is refused, before any device is looked for."""
+    calls = _load_calls()
+    cfg = RopeLayout(4, 2, 64).c()
+    with FakeTensorMode():
+        def cuda(*shape, dtype=torch.bfloat16):
+            return torch.empty(shape, dtype=dtype, device="cuda:0")
+
+        w, f = cuda(64), cuda(32, dtype=torch.float32)
+        rope = calls.Rope(ctypes.addressof(cfg), w, None, f, 0)
+        assert rope.q_weight is w and rope.k_weight is None and rope.inv_freq is f
+        with pytest.raises(AttributeError):
+            rope.q_weight = w
+    for bad in (1, "x"):
+        with pytest.raises(ValueError):
+            calls.Rope(ctypes.addressof(cfg), bad, None, None, 0)
+    lay = CacheLayout(4, 2, 64, page_size=16, n_pages=8).c()
+    k = torch.zeros(8, 2, 16, 64)
+    with pytest.raises(ValueError):
+        calls.Cache(ctypes.addressof(lay), (k,), (None, None), k, 0)
+    cache = calls.Cache(ctypes.addressof(lay), (k, k), (None, None), None, 0)
+    assert cache.k_pages is k and cache.k_exp is None and cache.workspace is None
+    # the objects give their references back, also in a circle
+    import gc
+    import sys
+    held = sys.getrefcount(k)
+    k.owner = cache
+    del cache, k.owner
+    gc.collect()
+    assert sys.getrefcount(k) == held - 2
+    cache = calls.Cache(ctypes.addressof(lay), (k, k), (None, None), None, 0)
+    k.owner = cache
+    ref = __import__("weakref").ref(k)
+    del k, cache
+    gc.collect()
+    assert ref() is None

@@ -1,5 +1,5 @@
 """The answering side at the edges of its ranges: small softmax weights of a
-quantised cache, lengths beyond the table, tensors without an address."""
+quantised cache, lengths beyond the table, tensors without an address or with another one."""
 import math
 
 import pytest
@@ -7,7 +7,7 @@ import torch
 
 import cache_util as cu
 from cache_util import E4M3
-from sequence_sparse_attention_b200 import CacheLayout, PagedCache, QKNormRope, RopeLayout
+from sequence_sparse_attention_b200 import CacheLayout, PagedCache, QKNormRope, RopeLayout, SpavaError
 
 pytestmark = pytest.mark.gpu
 
@@ -168,3 +168,55 @@ def test_transforms_raise_and_leave_the_process_and_the_calls_alone():
     cache.write(k[0], k[1], table, lens)
     got = cache.attn(q[0], table, lens)
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+# ------------------------------------------------------------------ kept tensors
+def test_replaced_memory_of_kept_tensors_is_followed():
+    """``.data`` of a weight, a table of frequencies, a pool or a workspace may be
+    replaced; the next call takes what is there then."""
+    Hq, Hkv, d, page, n = 4, 2, 64, 16, 3
+    g = gen(8)
+    w1, w2 = randn(d, g=g), randn(d, g=g)
+    f1, f2 = (torch.rand(d // 2, generator=g, device="cuda") for _ in range(2))
+    q, k = randn(n, Hq, d, g=g), randn(n, Hkv, d, g=g)
+    pos = torch.arange(5, 5 + n, dtype=torch.int32, device="cuda")
+    lay = RopeLayout(Hq, Hkv, d)
+    want = [QKNormRope(lay, f, w, w).apply(q, k, pos) for f, w in ((f1, w1), (f2, w2))]
+    w, f = torch.nn.Parameter(w1.clone(), requires_grad=False), f1.clone()
+    rope = QKNormRope(lay, f, w, w)
+    assert rope.q_weight is w
+    old = [w.data, f.data]
+    for i in (0, 1):
+        assert all(torch.equal(a, b) for a, b in zip(rope.apply(q, k, pos), want[i]))
+        w.data, f.data = w2.clone(), f2.clone()
+        del old[:]
+    w.data = w2.float()
+    with pytest.raises(ValueError):
+        rope.apply(q, k, pos)
+    w.data = w2.cpu()
+    with pytest.raises(ValueError):
+        rope.apply(q, k, pos)
+    w.data, f.data = w2, f2[:5]
+    with pytest.raises(ValueError):
+        rope.apply(q, k, pos)
+
+    for dtype in (BF16, E4M3):
+        lay = CacheLayout(Hq, Hkv, d, page_size=page, n_pages=4, dtype=dtype)
+        cache, other = PagedCache(lay), PagedCache(lay)
+        table, lens = torch.tensor([[1, 3]], dtype=torch.int32, device="cuda"), lengths(n)
+        cache.write(k, k, table, lens)
+        other.write(-k, -k, table, lens)
+        for t, x in zip((*cache.tensors, cache.workspace), (*other.tensors, other.workspace)):
+            t.data = x.clone()
+        got = cache.read(table, lens, n)
+        assert all(torch.equal(a, b) for a, b in zip(got, other.read(table, lens, n)))
+        assert torch.equal(cache.attn(q[:1], table, lens)[0], other.attn(q[:1], table, lens)[0])
+        cache.attn(q[:1], table, lengths(-1))
+        assert cache.device_status() == 2 and other.device_status() == 0
+        cache.k_pages.data = cache.k_pages[:2]
+        with pytest.raises(ValueError):
+            cache.write(k, k, table, lens)
+        cache.k_pages.data = other.k_pages
+        cache.workspace.data = cache.workspace[:256]
+        with pytest.raises(SpavaError):
+            cache.attn(q[:1], table, lens)
