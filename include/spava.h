@@ -418,7 +418,8 @@ typedef struct {
 /* A batch of sequences, all DEVICE memory (so that a captured graph can be
  * replayed with other contents): table int32 [n_seqs, max_pages] and lens int32
  * [n_seqs], the tokens of each sequence, new ones included.  max_pages >= 1,
- * max_pages * page_size <= 2^31 - 2^16, n_seqs < 2^20.  Table entries behind the last
+ * max_pages * page_size <= 2^31 - 2^16, n_seqs < 2^20; without sequences nothing is done
+ * (table, lens and the rows' buffers may be NULL).  Table entries behind the last
  * page of a sequence may hold anything.  Sequences may share pages.  A length below
  * 0 counts as 0; of one beyond the table, what lies behind the table is neither
  * read nor written; a page outside the pool is neither read nor written, its

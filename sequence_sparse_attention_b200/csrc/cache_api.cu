@@ -88,7 +88,7 @@ spava_status make_view(const spava_cache_config *c, const spava_cache_pools *p,
         SPAVA_TRY(check_ptr(p->k_exp));
         SPAVA_TRY(check_ptr(p->v_exp));
     }
-    if (!b->table || !b->lens) return SPAVA_ERR_INVALID_ARG;
+    if (b->n_seqs > 0 && (!b->table || !b->lens)) return SPAVA_ERR_INVALID_ARG;
     if ((reinterpret_cast<uintptr_t>(b->table) & 3) || (reinterpret_cast<uintptr_t>(b->lens) & 3))
         return SPAVA_ERR_MISALIGNED;
     if (!ws) return SPAVA_ERR_WORKSPACE;

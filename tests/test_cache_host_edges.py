@@ -6,7 +6,7 @@ import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
 
-from sequence_sparse_attention_b200 import CacheLayout, PagedCache, QKNormRope, RopeLayout
+from sequence_sparse_attention_b200 import CacheLayout, PagedCache, QKNormRope, RopeLayout, native
 from sequence_sparse_attention_b200.cache import _load_calls
 
 
@@ -76,3 +76,29 @@ def test_compiled_calls_keep_tensors_not_addresses():
     del k, cache
     gc.collect()
     assert ref() is None
+
+
+# ------------------------------------------------------------------ empty batches
+def test_an_empty_batch_needs_no_addresses():
+    """Tensors without elements have none."""
+    lib = native.load()
+    buf = ctypes.create_string_buffer(4096)
+    at = (ctypes.addressof(buf) + 255) // 256 * 256      # never dereferenced on these paths
+    lay = CacheLayout(4, 2, 64, page_size=16, n_pages=8).c()
+    rope = RopeLayout(4, 2, 64).c()
+    pools = native.SpavaCachePools(at, at, None, None)
+    end = (at, 1 << 40, None)
+
+    def calls(batch, rows=1):
+        h = ctypes.byref(lay), ctypes.byref(pools), ctypes.byref(batch)
+        return [lib.spava_cache_write(*h, rows, None, 128, None, 128, *end),
+                lib.spava_cache_append(ctypes.byref(rope), *h, rows, None, 256, None, 128, None, 128, None, None, None, None,
+                                       None, *end),
+                lib.spava_cache_read(*h, 0, rows, None, None, *end), lib.spava_cache_attn(*h, None, None, None, *end)]
+
+    assert calls(native.SpavaCacheBatch(0, 3, None, None)) == [0] * 4
+    assert calls(native.SpavaCacheBatch(0, 3, None, None), rows=0) == [0] * 4
+    # the rest of the arguments are looked at all the same
+    assert calls(native.SpavaCacheBatch(0, 0, None, None)) == [1] * 4
+    assert calls(native.SpavaCacheBatch(2, 3, None, at)) == [1] * 4
+    assert calls(native.SpavaCacheBatch(2, 3, at, None)) == [1] * 4

@@ -1,5 +1,6 @@
 """The answering side at the edges of its ranges: small softmax weights of a
-quantised cache, lengths beyond the table, tensors without an address or with another one."""
+quantised cache, lengths beyond the table, tensors without an address or with
+another one, empty batches."""
 import math
 
 import pytest
@@ -220,3 +221,23 @@ def test_replaced_memory_of_kept_tensors_is_followed():
         cache.workspace.data = cache.workspace[:256]
         with pytest.raises(SpavaError):
             cache.attn(q[:1], table, lens)
+
+
+# ------------------------------------------------------------------ empty batches
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_an_empty_batch_does_nothing(kind):
+    Hq, Hkv, d = 4, 2, 64
+    cache = PagedCache(CacheLayout(Hq, Hkv, d, page_size=16, n_pages=4, dtype=BF16 if kind == "bf16" else E4M3))
+    rope = QKNormRope(RopeLayout(Hq, Hkv, d), torch.ones(d // 2, device="cuda"))
+    table, lens = torch.zeros((2, 3), dtype=torch.int32, device="cuda")[:0], lengths(1, 2)[:0]
+    q, k = randn(2, Hq, d, g=gen())[:0], randn(2, Hkv, d, g=gen())[:0]
+    pos = torch.empty((1, 0), dtype=torch.int32, device="cuda")
+    assert [x.shape for x in rope.apply(q, k, pos)] == [(0, Hq, d), (0, Hkv, d)]
+    cache.write(k, k, table, lens)
+    assert cache.append(rope, q, k, k, pos, table, lens).shape == (0, Hq, d)
+    assert [x.shape for x in cache.read(table, lens, 7)] == [(0, 7, Hkv, d)] * 2
+    o, lse = cache.attn(q, table, lens)
+    assert o.shape == (0, Hq, d) and lse.shape == (Hq, 0)
+    assert not any(x.view(torch.uint8).any() for x in cache.tensors) and cache.device_status() == 0
+    with pytest.raises(ValueError):      # rows without a sequence
+        cache.write(randn(1, Hkv, d, g=gen()), randn(1, Hkv, d, g=gen()), table, lens)
