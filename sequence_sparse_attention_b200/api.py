@@ -198,12 +198,9 @@ class Spava:
                     _ptr(lse), _ptr(self.ws), self.ws.numel(), _stream(self.device), cs)
 
     def device_status(self) -> int:
-        """Synchronises, returns and clears the kernels' status word (0 = clean)."""
-        flags = ctypes.c_int32()
-        lib = native.load()
-        lib.spava_device_status(_ptr(self.ws), self.ws.numel(), _stream(self.device),
-                                ctypes.byref(flags))
-        return flags.value
+        """Synchronises, returns and clears the kernels' status word (0 = clean);
+        raises where it cannot be read."""
+        return native.device_status(self.ws, _stream(self.device))
 
 
 # ------------------------------------------------------------------ shards

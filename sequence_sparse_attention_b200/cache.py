@@ -205,11 +205,9 @@ class PagedCache:
 
     def device_status(self, workspace=None) -> int:
         """Synchronises, returns and clears the status word: bit 1 is a length
-        beyond its table or a page outside the pool (0 = clean)."""
-        flags = ctypes.c_int32()
+        beyond its table or a page outside the pool (0 = clean).  Raises where
+        the word cannot be read."""
         ws = self.workspace if workspace is None else workspace
         _check(ws, (ws.numel(),), torch.uint8, self.device.index, "workspace")
         with torch.cuda.device(self.device):
-            native.load().spava_device_status(ws.data_ptr(), ws.numel(),
-                                              torch.cuda.current_stream(self.device).cuda_stream, ctypes.byref(flags))
-        return flags.value
+            return native.device_status(ws, torch.cuda.current_stream(self.device).cuda_stream)

@@ -144,3 +144,14 @@ def call(name: str, *args) -> None:
     rc = getattr(lib, name)(*args)
     if rc != SPAVA_OK:
         raise SpavaError(name, rc, lib.spava_last_cuda_error() if rc == 5 else 0)
+
+
+def device_status(ws, stream: int) -> int:
+    """Reads and clears the status word of a workspace tensor (0: clean); raises
+    where it could not be read."""
+    flags = ctypes.c_int32()
+    lib = load()
+    rc = lib.spava_device_status(ws.data_ptr(), ws.numel(), stream, ctypes.byref(flags))
+    if rc != SPAVA_OK and flags.value == 0:      # with flags, the status says which
+        raise SpavaError("spava_device_status", rc, lib.spava_last_cuda_error() if rc == 5 else 0)
+    return flags.value

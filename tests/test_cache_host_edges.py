@@ -6,7 +6,7 @@ import pytest
 import torch
 from torch._subclasses.fake_tensor import FakeTensorMode
 
-from sequence_sparse_attention_b200 import CacheLayout, PagedCache, QKNormRope, RopeLayout, native
+from sequence_sparse_attention_b200 import CacheLayout, PagedCache, QKNormRope, RopeLayout, Spava, native
 from sequence_sparse_attention_b200.cache import _load_calls
 
 
@@ -102,3 +102,38 @@ def test_an_empty_batch_needs_no_addresses():
     assert calls(native.SpavaCacheBatch(0, 0, None, None)) == [1] * 4
     assert calls(native.SpavaCacheBatch(2, 3, None, at)) == [1] * 4
     assert calls(native.SpavaCacheBatch(2, 3, at, None)) == [1] * 4
+
+
+# ------------------------------------------------------------------ the status word
+@pytest.mark.parametrize("status,flags,want", [(0, 0, 0), (1, 2, 2), (6, 1, 1), (6, 3, 3), (5, 0, None), (1, 0, None)])
+def test_a_status_that_cannot_be_read_raises(monkeypatch, status, flags, want):
+    """A workspace that is too short or a CUDA error is not a clean status word."""
+    import contextlib
+    import types
+
+    class Lib:
+        def spava_device_status(self, ws, size, stream, to):
+            to._obj.value = flags
+            return status
+
+        def spava_last_cuda_error(self):
+            return 700
+
+        def spava_status_string(self, s):
+            return b"a status"
+
+    monkeypatch.setattr(native, "load", lambda: Lib())
+    stream = types.SimpleNamespace(cuda_stream=0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: stream)
+    monkeypatch.setattr(torch.cuda, "device", lambda *a: contextlib.nullcontext())
+    ws = torch.zeros(256, dtype=torch.uint8)
+    device = types.SimpleNamespace(index=-1)
+    for read in (lambda: PagedCache.device_status(types.SimpleNamespace(workspace=ws, device=device)),
+                 lambda: PagedCache.device_status(types.SimpleNamespace(workspace=None, device=device), workspace=ws),
+                 lambda: Spava.device_status(types.SimpleNamespace(ws=ws, device=device))):
+        if want is not None:
+            assert read() == want
+            continue
+        with pytest.raises(native.SpavaError) as e:
+            read()
+        assert e.value.status == status and e.value.cuda_error == (700 if status == 5 else 0)

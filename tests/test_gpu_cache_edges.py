@@ -241,3 +241,12 @@ def test_an_empty_batch_does_nothing(kind):
     assert not any(x.view(torch.uint8).any() for x in cache.tensors) and cache.device_status() == 0
     with pytest.raises(ValueError):      # rows without a sequence
         cache.write(randn(1, Hkv, d, g=gen()), randn(1, Hkv, d, g=gen()), table, lens)
+
+
+# ------------------------------------------------------------------ the status word
+def test_a_short_workspace_has_no_clean_status():
+    cache = PagedCache(CacheLayout(4, 2, 64, page_size=16, n_pages=4))
+    assert cache.device_status() == 0 == cache.device_status(workspace=cache.new_workspace())
+    with pytest.raises(SpavaError) as e:
+        cache.device_status(workspace=torch.zeros(255, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == 1
