@@ -15,7 +15,9 @@ constexpr int kStatusBadBatch = 2;
 // CUDA error code of this thread's last SPAVA_ERR_CUDA (spava_last_cuda_error).
 inline thread_local int32_t g_last_cuda_error = 0;
 
+// Also takes the error from the runtime, which would give it to the next launched().
 inline spava_status cuda_fail(cudaError_t e) {
+    cudaGetLastError();
     g_last_cuda_error = static_cast<int32_t>(e);
     return SPAVA_ERR_CUDA;
 }

@@ -137,3 +137,35 @@ def test_a_status_that_cannot_be_read_raises(monkeypatch, status, flags, want):
         with pytest.raises(native.SpavaError) as e:
             read()
         assert e.value.status == status and e.value.cuda_error == (700 if status == 5 else 0)
+
+
+# ------------------------------------------------------------------ errors of the runtime
+def test_a_refused_call_leaves_no_error_behind(tmp_path):
+    """The runtime remembers a call's error until it is asked: left there, the next
+    launch that is checked by asking would report it as its own.  The helpers are
+    compiled with a runtime of four lines."""
+    import os
+    import subprocess
+
+    from sequence_sparse_attention_b200 import build
+    (tmp_path / "t.cpp").write_text(r'''
+#include "status.cuh"
+static cudaError_t pending = cudaSuccess;
+extern "C" cudaError_t cudaGetLastError() { cudaError_t e = pending; pending = cudaSuccess; return e; }
+static cudaError_t refused() { return pending = cudaErrorLaunchOutOfResources; }
+static spava_status macro() { SPAVA_CUDA(refused()); return SPAVA_OK; }
+int main() {
+    using namespace spava;
+    if (cuda_ok(refused()) != SPAVA_ERR_CUDA || g_last_cuda_error != cudaErrorLaunchOutOfResources) return 1;
+    if (launched() != SPAVA_OK) return 2;   // a launch that was fine
+    if (macro() != SPAVA_ERR_CUDA) return 3;
+    if (launched() != SPAVA_OK) return 4;
+    refused();                              // one that was not
+    if (launched() != SPAVA_ERR_CUDA || g_last_cuda_error != cudaErrorLaunchOutOfResources) return 5;
+    return launched() == SPAVA_OK ? 0 : 6;
+}
+''')
+    cuda = os.path.dirname(os.path.dirname(build.nvcc()))
+    subprocess.check_call(["g++", "-std=c++17", "-I" + os.path.join(cuda, "include"), "-I" + build.CSRC,
+                           str(tmp_path / "t.cpp"), "-o", str(tmp_path / "t")])
+    assert subprocess.run([str(tmp_path / "t")]).returncode == 0
