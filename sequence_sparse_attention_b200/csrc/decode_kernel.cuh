@@ -348,7 +348,7 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
 
         // ---- q: the MMA's B operand, and its scale
         uint32_t qf[NT][S::KS][2];
-        float q_scale[NT][2];  // of the heads 2c and 2c+1 of this lane's accumulators
+        float q_scale[NT][2];  // of the heads 2c and 2c+1 of this lane's accumulators (e4m3: its root)
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
             const int h = t * 8 + g;
@@ -368,8 +368,10 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
                 for (int i = 0; i < S::KS; ++i) qf[t][i][0] = w[i][0], qf[t][i][1] = w[i][1];
                 q_scale[t][0] = q_scale[t][1] = p.scale_log2;
             } else {
-                // q as fp16 times 2^x, x from the row's largest magnitude: what
-                // fp16 cannot hold of it is below 2^-24 of that.
+                // q as fp16 times 2^-x, x even and from the row's largest magnitude:
+                // what fp16 cannot hold of it is below 2^-24 of that.  The score takes
+                // 2^(x/2) before and behind the key's scale: exponents may lie at
+                // opposite ends of the range and their sum in the middle.
                 float m = 0.f;
 #pragma unroll
                 for (int i = 0; i < S::KS; ++i)
@@ -378,17 +380,16 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
                         m = fmaxf(m, fmaxf(fabsf(bf_lo(w[i][k])), fabsf(bf_hi(w[i][k]))));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
                 m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-                const int x = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -100), 127);
-                // 2^-127 is no normal number: in two steps
-                const float f0 = pow2f(-(x / 2)), f1 = pow2f(-(x - x / 2));
+                const int x = min(max(static_cast<int>(__float_as_uint(m) >> 23) - 127, -126), 127) & ~1;
+                const float f = pow2f(-x / 2);
 #pragma unroll
                 for (int i = 0; i < S::KS; ++i)
 #pragma unroll
                     for (int k = 0; k < 2; ++k)
-                        qf[t][i][k] = pack_half2(bf_lo(w[i][k]) * f0 * f1, bf_hi(w[i][k]) * f0 * f1);
+                        qf[t][i][k] = pack_half2(bf_lo(w[i][k]) * f * f, bf_hi(w[i][k]) * f * f);
                 const int xa = __shfl_sync(0xffffffffu, x, 8 * c), xb = __shfl_sync(0xffffffffu, x, 8 * c + 4);
-                q_scale[t][0] = p.scale_log2 * pow2f(xa);
-                q_scale[t][1] = p.scale_log2 * pow2f(xb);
+                q_scale[t][0] = sqrtf(p.scale_log2) * pow2f(xa / 2);
+                q_scale[t][1] = sqrtf(p.scale_log2) * pow2f(xb / 2);
             }
         }
 
@@ -490,8 +491,8 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         float x = s[sb][t][k];
-                        if (E4M3) x *= kf[k / 2];
                         x *= q_scale[t][k % 2];
+                        if (E4M3) x = x * kf[k / 2] * q_scale[t][k % 2];
                         if (!((bits >> (g + 8 * (k / 2))) & 1)) x = -INFINITY;
                         s[sb][t][k] = x;
                         grow |= x > l_ref[t][k % 2] + kDecLag;

@@ -1,6 +1,6 @@
 """The answering side at the edges of its ranges: small softmax weights of a
 quantised cache, lengths beyond the table, tensors without an address or with
-another one, empty batches."""
+another one, empty batches, exponents at the ends of bf16."""
 import math
 
 import pytest
@@ -250,3 +250,23 @@ def test_a_short_workspace_has_no_clean_status():
     with pytest.raises(SpavaError) as e:
         cache.device_status(workspace=torch.zeros(255, dtype=torch.uint8, device="cuda"))
     assert e.value.status == 1
+
+
+# ------------------------------------------------------------------ extreme exponents
+@pytest.mark.parametrize("k_exp,q_exp", [(124, -124), (124, -130), (100, -108), (-124, 124), (-133, 126), (60, -60)])
+@pytest.mark.parametrize("tokens", [20, 900, 20000])
+def test_scores_of_opposite_exponents(k_exp, q_exp, tokens):
+    """Keys and queries next to the ends of bf16, products of ordinary size: the
+    scores are those of the products."""
+    Hq, Hkv, d, page = 4, 2, 64, 16
+    g = gen(tokens)
+    k, v = randn(tokens, Hkv, d, g=g), randn(tokens, Hkv, d, g=g)
+    k = torch.ldexp(k.float(), torch.tensor(k_exp, device="cuda")).to(BF16)
+    q = torch.ldexp(randn(1, Hq, d, g=g).float(), torch.tensor(q_exp, device="cuda")).to(BF16)
+    assert k.isfinite().all() and k.any() and q.any()
+    pages = -(-tokens // page)
+    cache = PagedCache(CacheLayout(Hq, Hkv, d, page_size=page, n_pages=pages, dtype=E4M3))
+    table, lens = cu.make_table(1, pages, pages, g), lengths(tokens)
+    cache.write(k, v, table, lens)
+    o, lse = cache.attn(q, table, lens)
+    cu.check_attn(o, lse, q, cache.tensors, table, [tokens], page)
