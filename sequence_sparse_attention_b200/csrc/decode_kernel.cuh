@@ -149,14 +149,23 @@ __device__ __forceinline__ void store_lse(const DecodeParams &p, int b, int head
         p.lse[static_cast<int64_t>(head) * p.cache.n_seqs + b] =
             l == 0.f ? -INFINITY : 0.6931471805599453f * (lm + log2f(l));
 }
+// The output's element of O's: times 2^(m - lm), over l.  Their product may lie below the normal range
+// where neither they nor the output do (values of 2^-117, many tokens), so they are
+// applied one after the other.
+struct OutputScale {
+    float inv, pow;
+    __device__ __forceinline__ OutputScale(float m, float lm, float l)
+        : inv(l == 0.f ? 0.f : 1.f / l), pow(l == 0.f ? 0.f : exp2f(m - lm)) {}
+    __device__ __forceinline__ float operator()(float o) const { return o * inv * pow; }
+};
 // Four elements of a query head's output, and with the first its lse, from the
 // whole context's state.
 template <int D>
 __device__ __forceinline__ void store_result(const DecodeParams &p, int b, int head, int d, float m, float lm,
                                              float l, const float4 &o) {
-    const float f = l == 0.f ? 0.f : exp2f(m - lm) / l;
+    const OutputScale f(m, lm, l);
     *reinterpret_cast<uint2 *>(p.o + (static_cast<int64_t>(b) * p.Hq + head) * D + d) =
-        make_uint2(bf_pack(o.x * f, o.y * f), bf_pack(o.z * f, o.w * f));
+        make_uint2(bf_pack(f(o.x), f(o.y)), bf_pack(f(o.z), f(o.w)));
     if (d == 0) store_lse(p, b, head, lm, l);
 }
 
@@ -649,12 +658,12 @@ __device__ __forceinline__ void decode_body(const DecodeParams &p) {
 #pragma unroll
                     for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
                     if (h >= n_heads) continue;
-                    const float f = l == 0.f ? 0.f : exp2f(m_ref[t][k] - l_ref[t][k]) / l;
+                    const OutputScale f(m_ref[t][k], l_ref[t][k], l);
                     __nv_bfloat16 *to = p.o + (static_cast<int64_t>(b) * p.Hq + head0 + h) * D;
 #pragma unroll
                     for (int i = 0; i < S::MT; ++i)
                         *reinterpret_cast<uint32_t *>(to + S::column(i, g)) =
-                            bf_pack(acc[t][i][k] * f, acc[t][i][2 + k] * f);
+                            bf_pack(f(acc[t][i][k]), f(acc[t][i][2 + k]));
                     if (g == 0) store_lse(p, b, head0 + h, l_ref[t][k], l);
                 }
             return;

@@ -270,3 +270,19 @@ def test_scores_of_opposite_exponents(k_exp, q_exp, tokens):
     cache.write(k, v, table, lens)
     o, lse = cache.attn(q, table, lens)
     cu.check_attn(o, lse, q, cache.tensors, table, [tokens], page)
+
+
+@pytest.mark.parametrize("tokens", [20, 900, 131072])
+def test_outputs_next_to_the_smallest(tokens):
+    """Values of 2^-117: the average of many keeps its bits."""
+    Hq, Hkv, d, page = 4, 2, 64, 16
+    g = gen(tokens)
+    k, v = randn(tokens, Hkv, d, g=g, scale=0.1), randn(tokens, Hkv, d, g=g).abs()
+    v = torch.ldexp(v.float(), torch.tensor(-117, device="cuda")).to(BF16)
+    q = randn(1, Hq, d, g=g)
+    pages = -(-tokens // page)
+    cache = PagedCache(CacheLayout(Hq, Hkv, d, page_size=page, n_pages=pages, dtype=E4M3))
+    table, lens = cu.make_table(1, pages, pages, g), lengths(tokens)
+    cache.write(k, v, table, lens)
+    o, lse = cache.attn(q, table, lens)
+    cu.check_attn(o, lse, q, cache.tensors, table, [tokens], page)
