@@ -1,6 +1,6 @@
 """The answering side at the edges of its ranges: small softmax weights of a
 quantised cache, lengths beyond the table, tensors without an address or with
-another one, empty batches, exponents at the ends of bf16."""
+another one, empty batches, exponents at the ends of bf16, blocks full of tokens."""
 import math
 
 import pytest
@@ -286,3 +286,71 @@ def test_outputs_next_to_the_smallest(tokens):
     cache.write(k, v, table, lens)
     o, lse = cache.attn(q, table, lens)
     cu.check_attn(o, lse, q, cache.tensors, table, [tokens], page)
+
+
+# ------------------------------------------------------------------ blocks of many tokens
+def full_pools(e4m3, *shape):
+    out = [torch.zeros(shape, dtype=torch.uint8 if e4m3 else BF16, device="cuda") for _ in range(2)]
+    if e4m3:
+        return [x.view(E4M3) for x in out] + [torch.zeros(shape[:3], dtype=torch.int8, device="cuda") for _ in range(2)]
+    return out + [None, None]
+
+
+def check_pools(pools, k, v, table, lens, page, new):
+    """Pools that held zeros, after a write of k and v [sequences * new, Hkv, d]."""
+    n = len(lens)
+    pos = torch.tensor(lens, device="cuda")[:, None] - new + torch.arange(new, device="cuda")
+    p, r = table.long().gather(1, pos // page).flatten(), (pos % page).flatten()
+    for i, x in enumerate((k, v)):
+        vals, exps = (x.double(), None) if pools[2] is None else cu.quantise(x)
+        assert torch.equal(pools[i][p, :, r].double(), vals)
+        if exps is not None:
+            assert torch.equal(pools[2 + i][p, :, r].double(), exps)
+        rest = pools[i].view(torch.uint8).clone()
+        rest[p, :, r] = 0
+        assert not rest.any()
+    assert len({*zip(p.tolist(), r.tolist())}) == n * new
+
+
+# Rows around the thresholds from which a block takes twice the tokens (2368, 4736,
+# ... rows), up to 32 of them, with a remainder in the last block.
+MANY = [(2369, 28, 4, 128), (4737, 28, 4, 128), (38001, 28, 4, 128), (18945, 2, 1, 64), (75777, 2, 1, 64), (9473, 4, 2, 128),
+        (5001, 40, 8, 64), (35, 1, 1, 64)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows,Hq,Hkv,d", MANY)
+def test_blocks_of_many_tokens(rows, Hq, Hkv, d, kind):
+    """Norm with rotation, append, write and read of as many rows as a prefill has."""
+    e4m3, page = kind == "e4m3", 48
+    g = gen(rows)
+    qkv = randn(rows, (Hq + 2 * Hkv) * d, g=g)
+    q, k, v = (x.unflatten(1, (-1, d)) for x in qkv.split([Hq * d, Hkv * d, Hkv * d], 1))
+    pos = torch.randint(0, 1 << 20, (2, rows), generator=g, device="cuda", dtype=torch.int32)
+    sections, freq = (d // 8, d // 2 - d // 8), (1e6 ** (-torch.arange(d // 2, device="cuda") / (d // 2))).float()
+    qw, kw = randn(d, g=g), randn(d, g=g)
+    rope = QKNormRope(RopeLayout(Hq, Hkv, d, sections=sections), freq, qw, kw)
+    qo, ko = rope.apply(q, k, pos)
+    for got, x, w in ((qo, q, qw), (ko, k, kw)):
+        cu.check_norm_rope(got, cu.norm_rope(x, w, pos, freq, d, False, sections, True, 1e-6))
+    # the rows as those of one sequence, or of as many as divide them
+    n = next(n for n in (7, 5, 3, 1) if rows % n == 0)
+    new = rows // n
+    per = -(-(new + 11) // page)
+    table = cu.make_table(n, per, n * per + 2, g)
+    lens = [new + 11 - b for b in range(n)]
+    for call in ("write", "append"):
+        pools = full_pools(e4m3, n * per + 2, Hkv, page, d)
+        cache = PagedCache(CacheLayout(Hq, Hkv, d, page_size=page, n_pages=n * per + 2, dtype=pools[0].dtype),
+                           k_pages=pools[0], v_pages=pools[1], k_exp=pools[2], v_exp=pools[3])
+        if call == "write":
+            cache.write(ko, v, table, lengths(*lens))
+        else:
+            assert torch.equal(cache.append(rope, q, k, v, pos, table, lengths(*lens)), qo)
+        check_pools(pools, ko, v, table, lens, page, new)
+    kr, vr = cache.read(table, lengths(*lens), new + 13, first=1)
+    for b, m in enumerate(lens):
+        ks, vs = cu.rows_of(pools, table, b, m, page)
+        for got, ref in ((kr, ks), (vr, vs)):
+            assert torch.equal(got[b, :m - 1].double(), ref[1:]) and not got[b, m - 1:].any()
+    assert cache.device_status() == 0
