@@ -77,10 +77,12 @@ at::Tensor output(PyObject *given, at::IntArrayRef shape, at::ScalarType type, i
     return at::detail::empty_cuda(shape, type, at::Device(at::kCUDA, static_cast<c10::DeviceIndex>(index)), std::nullopt);
 }
 
-// Raises for a tensor without memory of its own (a transform's or a fake one).
+// Raises for a tensor without memory of its own: a transform's or a fake one, one
+// whose storage was given back.
 void *ptr(const at::Tensor &t, const char *name) {
     void *p = t.data_ptr();
-    if (!t.storage().device().is_cuda()) throw Refused{c10::str(name, ": expected a tensor with memory, got ", said(t))};
+    if (!t.storage().device().is_cuda() || (t.storage().nbytes() == 0 && t.numel() != 0))
+        throw Refused{c10::str(name, ": expected a tensor with memory, got ", said(t))};
     return p;
 }
 

@@ -354,3 +354,20 @@ def test_blocks_of_many_tokens(rows, Hq, Hkv, d, kind):
         for got, ref in ((kr, ks), (vr, vs)):
             assert torch.equal(got[b, :m - 1].double(), ref[1:]) and not got[b, m - 1:].any()
     assert cache.device_status() == 0
+
+
+def test_tensors_whose_memory_was_given_back_are_refused():
+    """A weight without its storage is not a missing weight, whose place ones take."""
+    g = gen(9)
+    q, k, w = randn(3, 4, 64, g=g), randn(3, 2, 64, g=g), randn(64, g=g)
+    rope = QKNormRope(RopeLayout(4, 2, 64, rope_dim=0), None, w, w)
+    rope.apply(q, k)
+    w.untyped_storage().resize_(0)
+    with pytest.raises(ValueError):
+        rope.apply(q, k)
+    cache = PagedCache(CacheLayout(4, 2, 64, page_size=16, n_pages=4))
+    table, lens = cu.make_table(1, 2, 4, g), lengths(3)
+    cache.write(k, k, table, lens)
+    cache.v_pages.untyped_storage().resize_(0)
+    with pytest.raises(ValueError):
+        cache.read(table, lens, 3)
