@@ -474,8 +474,10 @@ spava_status spava_cache_read(const spava_cache_config *cfg, const spava_cache_p
  *   o[b, h] = sum_t softmax_t(scale * q[b, h] . k[t, h / (Hq/Hkv)]) v[t]
  * o [n_seqs, Hq, d] bf16; lse (may be NULL) float32 [Hq, n_seqs], natural log:
  * with it, partial results over parts of a context can be merged.  A sequence
- * without positions gives o = 0 and lse = -inf.  Positions past lens[b] are
- * never read, whatever they hold.  Several new tokens of one sequence are
+ * without positions gives o = 0 and lse = -inf.  Scores, sums and outputs are
+ * held in 32 bits; the softmax weights enter the product with the values with 16
+ * significant bits (22 over an e4m3 cache) and o is rounded once.  Positions past
+ * lens[b] are never read, whatever they hold.  Several new tokens of one sequence are
  * several rows of the batch, with the same table row and growing lens.
  * Results do not depend on timing: the same call gives the same bytes.
  * SPAVA_ERR_UNSUPPORTED if the tables hold 2^31 work units or more (a unit is

@@ -116,7 +116,7 @@ spava_status make_view(const spava_cache_config *c, const spava_cache_pools *p,
 // pass, then more where there are plenty, as a block's tokens share what it makes
 // for them; few tokens are spread over the SMs head by head.  (Norm, rotation and
 // write of 64 tokens, 48 heads: 3.1 us, 10.5 with eight tokens a block and no
-// sharing out.  Norm of 131072 tokens: 353 us, 370 with four tokens a block; of 5000:
+// sharing out.  Norm of 131072 tokens: 350 us, 363 with four tokens a block; of 5000:
 // 18.4 us, 20.8 where half as many blocks are plenty.)
 void split_tokens(int64_t n_rows, int64_t heads, int most, int per_pass, int32_t *tokens_log2, int64_t *splits) {
     constexpr int kBlocks = 148 * 4;  // enough to fill the SMs
@@ -201,8 +201,8 @@ bool by_clusters(int64_t blocks, int64_t kib) { return kib <= 256 && kib * (130 
 // (8 KiB of K and V rows): always up to two, up to 8 where there are too many items
 // for clusters, up to 16 where there are many more.  By the line or clusters / by
 // warps, device time in us: one sequence of 32 tokens, 4 KV heads, bf16 4.3 / 3.2
-// (of 64, four tiles, 4.4 / 4.4); 100 sequences of 64, 8 KV heads, e4m3 13.2 / 5.6;
-// 40 of 500 (320 items, 16 tiles) 16.6 / 22.7, 100 (800 items) 28.5 / 24.0.
+// (of 64, four tiles, 4.4 / 4.4); 100 sequences of 64, 8 KV heads, e4m3 13.8 / 6.1;
+// 40 of 500 (320 items, 16 tiles) 17.2 / 23.4, 100 (800 items) 29.5 / 26.3.
 bool by_warps(int64_t tiles, int64_t items, int64_t slots) {
     return tiles <= (items <= slots ? 2 : items < 2 * slots ? 8 : 16);
 }

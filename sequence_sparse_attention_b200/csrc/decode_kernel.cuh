@@ -188,8 +188,8 @@ struct DecodeShape {
     static constexpr int HEADS = 8 * NT;
     // The low products of an e4m3 cache have accumulators of their own where the
     // registers hold them; else the values are made kDecLow times smaller for them,
-    // which is exact in fp16 (512 sequences of 2000 tokens, 4 heads a KV head: 326 us,
-    // 348 with smaller values; two tiles of heads would spill).
+    // which is exact in fp16 (512 sequences of 2000 tokens, 4 heads a KV head: 327 us,
+    // 348 with smaller values; two tiles of heads are at 255 registers without).
     static constexpr bool APART = E4M3 && NT == 1;
     // The 16-byte pieces of a row lie permuted (piece ^ swizzle) so that the
     // eight lanes that read at a time, pieces c of the K rows g, g + 1 or pieces
@@ -238,8 +238,8 @@ struct DecodeShape {
 //     products, 22 significant bits down to 2^-25 of the largest weight and steps of
 //     2^-42 of it below.  A row's scales come in as exponents: of K into the score,
 //     of V into P, whose reference m then covers score + exponent, while the sum
-//     l has its own, lm.  (One product, 11 bits: 512 sequences of 2000 tokens 320
-//     instead of 326 us.)
+//     l has its own, lm.  (One product, 11 bits: 512 sequences of 2000 tokens 325
+//     instead of 328 us.)
 //   - The work of the whole batch is a line of units (BLOCK tokens of one
 //     sequence and KV head), cut into equal shares, one per block, by every
 //     block for itself from the lengths: long and short sequences balance, and
@@ -247,7 +247,7 @@ struct DecodeShape {
 //     of cut items in the workspace for join_kernel.
 //
 // Measured: 131072 tokens, 28/4 heads of 128, bf16, 48.0 us with the join, 5.6 TB/s;
-// 512 sequences of 2000 tokens, 32/8 heads, e4m3, 327 us.
+// 512 sequences of 2000 tokens, 32/8 heads, e4m3, 328 us.
 template <int D, bool E4M3, int NT, DecodeMode MODE>
 __device__ __forceinline__ void decode_body(const DecodeParams &p) {
     using S = DecodeShape<D, E4M3, NT>;
@@ -910,7 +910,7 @@ __global__ void __launch_bounds__(kDecThreads)
 
 // More items than the SMs hold blocks, and short contexts: an item is one warp's,
 // from its first tile to its result, without a barrier or a join: 500 sequences of 64
-// tokens, 32/8 heads of 128, e4m3, 21.5 us, 54 along the line.
+// tokens, 32/8 heads of 128, e4m3, 22.4 us, 56 along the line.
 template <int D, bool E4M3, int NT>
 __global__ void __launch_bounds__(kDecThreads) decode_warp_kernel(const __grid_constant__ DecodeParams p) {
     decode_body<D, E4M3, NT, DecodeMode::kWarp>(p);

@@ -125,8 +125,8 @@ __device__ __forceinline__ void turn2(float2 &a, float2 &b, float2 cs, float2 sn
 // any 31-bit position, where a 32-bit product is off by up to 2^-24 of the
 // angle itself (0.008 radians at position 131072).
 //
-// Measured, 28/4 heads of 128: 131072 tokens 353 us, 6.1 TB/s read and written (0.92
-// of the copy rate); 16384 tokens 48.8 us; e4m3 write of 16384 tokens, 4 KV heads,
+// Measured, 28/4 heads of 128: 131072 tokens 350 us, 6.1 TB/s read and written (0.93
+// of the copy rate); 16384 tokens 49.1 us; e4m3 write of 16384 tokens, 4 KV heads,
 // 10.8 us; one token with its write 2.7 us.
 //
 // ROPE: norm or rotation of queries and keys.  CACHE: 0 none, 1 bf16, 2 e4m3.
