@@ -65,6 +65,7 @@ def test_compiled_calls_keep_tensors_not_addresses():
     # the objects give their references back, also in a circle
     import gc
     import sys
+    import weakref
     held = sys.getrefcount(k)
     k.owner = cache
     del cache, k.owner
@@ -72,7 +73,7 @@ def test_compiled_calls_keep_tensors_not_addresses():
     assert sys.getrefcount(k) == held - 2
     cache = calls.Cache(ctypes.addressof(lay), (k, k), (None, None), None, 0)
     k.owner = cache
-    ref = __import__("weakref").ref(k)
+    ref = weakref.ref(k)
     del k, cache
     gc.collect()
     assert ref() is None
